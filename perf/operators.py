@@ -175,7 +175,7 @@ def _paged(s, case, kv, g, device):
         codes = torch.randn(pages, hk, page, dim, generator=g, device=device).mul_(36).round_().clamp_(-127, 127)
         s["c" + name] = codes.to(torch.int8)
         s["s" + name] = (0.5 + 1.5 * torch.rand(pages, hk, page // BLOCK, generator=g, device=device)) / 36
-    s.update(kv_len=_ints(kv, device), kv_most=max(kv), page=page)
+    s.update(kv_len=_ints(kv, device), page=page)
 
 
 def prepare(case, seed):
@@ -230,7 +230,7 @@ def _calls(s):
     cache = cr.KV8Cache(s["ck"], s["cv"], s["sk"], s["sv"])
     if op == "attn":
         return [cr.AttnKV8(s["q"], cache, s["table"], s["kv_len"], s["out"], cu=s["cu"], lse=s["lse"], scale=s["scale"],
-                           causal=s["causal"], max_kv=s["kv_most"])]
+                           causal=s["causal"])]
     if op == "read":
         return [cr.KV8Read(cache, s["table"], s["kv_len"], s["k_back"], s["v_back"], cu=s["cu"])]
     return [cr.KV8Append(s["q"], s["k"], s["v"], cache, s["table"], s["kv_len"], s["q_out"], cu=s["cu"], q_weight=s["qw"],
