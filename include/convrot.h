@@ -493,11 +493,209 @@ convrot_status_t convrot_embed_lookup(const int32_t *tokens, int64_t t, const in
                                       int64_t vocab, int64_t dim, void *out_bf16, void *stream);
 
 /*
+ * ---------------------------------------------------------------- attention beside the linears
+ * What a decoder layer needs between its q/k/v projections and its output
+ * projection: norms of queries and keys per head with the position rotation
+ * (convrot_qk_norm_rope), a paged key/value cache in INT8 that keys and
+ * values are appended to with norm and rotation on the way
+ * (convrot_kv8_append) and read back from (convrot_kv8_read), and attention
+ * over that cache (convrot_attn_kv8).  The source pages quantise the
+ * projections around them and have no passage on these; they are this
+ * library's extension.
+ *
+ * In all four, heads are rows of head_dim BF16 values; where a call takes
+ * strides (in elements: from token to token, from head to head) the rows may
+ * lie anywhere, a view of a joint q/k/v projection included, as long as
+ * every row starts on a 16-byte boundary (base aligned, strides multiples of
+ * 8).  Strides of inputs are not negative and may be 0; rows of outputs do
+ * not overlap.  head_dim is 64 or 128.
+ *
+ * The paged cache: a VIEW of caller-owned device memory.
+ *   k, v : int8 [pages, kv_heads, page_tokens, head_dim] codes
+ *   k_scale, v_scale : fp32 [pages, kv_heads, page_tokens / 16], one for
+ *           every block of 16 tokens of a page and head: a code stands for
+ *           code * scale
+ * page_tokens a power of two, 16 .. 1024.  Nothing needs to be initialised:
+ * only tokens that a call stored are ever used.
+ */
+typedef struct {
+    int8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages;
+    int32_t kv_heads, page_tokens, head_dim;
+} convrot_kv8_t;
+
+/* Fill a cache handle.  Checks: pointers non-NULL and 16-byte aligned, pages
+   1 .. 2^31 - 1, kv_heads 1 .. 4096, page_tokens and head_dim as above.  Host only. */
+convrot_status_t convrot_kv8_init(convrot_kv8_t *c, int8_t *k, int8_t *v, float *k_scale, float *v_scale,
+                                  int64_t pages, int32_t kv_heads, int32_t page_tokens, int32_t head_dim);
+
+/*
+ * The position rotation: the pairs (a, b) of a head's first rot_dim dims
+ * become (a c - b s, b c + a s) with (c, s) = cos_sin[position][pair].
+ *   cos_sin  : fp32 [positions, rot_dim / 2, 2] (device)
+ *   rot_dim  : a multiple of 8, 8 .. head_dim; the dims behind it stay
+ *   adjacent : 0: pair i is dims (i, i + rot_dim / 2);  1: dims (2 i, 2 i + 1)
+ *   axis     : uint8 [rot_dim / 2] (device): the row of `positions` that pair
+ *              i goes by (several position axes: time, height, width), or
+ *              NULL: row 0 for all
+ *   axes     : rows of the positions, 1 .. 8
+ * A position outside the table (or an axis >= axes) cannot be checked on the
+ * host: the row (a cached key included) is written as zeros and
+ * CONVROT_ERR_INVALID_ARG is recorded for convrot_device_status().
+ */
+typedef struct {
+    const float *cos_sin;
+    int64_t positions;
+    int32_t rot_dim, adjacent;
+    const uint8_t *axis;
+    int32_t axes;
+} convrot_rope_t;
+
+/*
+ * y = rotate(x * rsqrt(mean(x^2) + eps) * w) for every head of q
+ * [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim], in FP32
+ * with one rounding to BF16.
+ *   q_weight, k_weight : BF16 [head_dim] or NULL (that input is not normalised)
+ *   rope, positions    : int32 [rope->axes, tokens] (device), or rope NULL
+ *   kv_heads 0: no k.  q_out may be q and k_out may be k with equal strides
+ *   (in place); otherwise outputs overlap no input.
+ * At most 2^31 - 1 heads of tokens (tokens * (q_heads + kv_heads)).
+ */
+typedef struct {
+    int64_t tokens;
+    int32_t q_heads, kv_heads, head_dim;
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    const void *k;
+    int64_t k_token_stride, k_head_stride;
+    void *q_out;
+    int64_t q_out_token_stride, q_out_head_stride;
+    void *k_out;
+    int64_t k_out_token_stride, k_out_head_stride;
+    const void *q_weight, *k_weight;
+    float eps;
+    const convrot_rope_t *rope;
+    const int32_t *positions;
+} convrot_qk_norm_rope_t;
+convrot_status_t convrot_qk_norm_rope(const convrot_qk_norm_rope_t *job, void *stream);
+
+/*
+ * The sequences of a step, as the three cache calls take them:
+ *   page_table : int32 [batch, max_pages] (device): the pages of each
+ *                sequence's tokens in order; entries behind its last page are
+ *                not read
+ *   kv_len : int32 [batch] (device): cached tokens of each sequence, this
+ *            step's included
+ *   cu     : int32 [batch + 1] (device), not decreasing, cu[0] = 0: the rows
+ *            cu[b] .. cu[b + 1] - 1 of the step's tensors are the LAST tokens
+ *            of sequence b, at positions kv_len[b] - n .. kv_len[b] - 1; or
+ *            NULL: one row for each sequence (tokens == batch)
+ *   tokens : rows of the step's tensors.  Rows behind cu[batch] belong to no
+ *            sequence and are left as they were (a batch padded to a captured
+ *            size); so may whole sequences be empty.
+ * A row whose position would be negative (kv_len[b] < n, an idle slot of a
+ * captured batch) is padding: nothing is stored for it and its outputs are
+ * zeros.  What only the device can see to be wrong (a page outside the cache
+ * where one is needed, kv_len beyond max_pages * page_tokens, cu outside
+ * 0 .. tokens) is recorded as CONVROT_ERR_INVALID_ARG for
+ * convrot_device_status(); nothing is read or written out of bounds, tokens
+ * on such pages are not stored, read as zeros and not attended to.
+ */
+typedef struct {
+    const int32_t *page_table, *kv_len, *cu;
+    int64_t tokens;
+    int32_t batch, max_pages;
+} convrot_kv8_seqs_t;
+
+/*
+ * Append a step's keys and values to the cache: k [tokens, kv_heads,
+ * head_dim] normalised (k_weight non-NULL) and rotated, v as it is, each
+ * quantised from FP32 to INT8; q [tokens, q_heads, head_dim], normalised and
+ * rotated, goes to q_out in BF16 (q_heads 0: no q).  Norm and rotation as in
+ * convrot_qk_norm_rope; positions NULL: the position in the sequence (then
+ * rope->axes is 1 and rope->axis NULL).
+ *   codes  q = clamp(rne(x / s), -127, 127)
+ *   scale  of a block whose first token is among the new ones: s = max|x| /
+ *          127 over its new tokens.  Of a block that holds older tokens: s
+ *          stays if max|x| < 127.5 s; otherwise it doubles until that holds
+ *          and the older codes become rne(q / 2^j) -- a value is off by less
+ *          than one step of its block's final scale, however many calls
+ *          filled the block.
+ * The same call again stores the same.  No two sequences may append to one
+ * block (pages that sequences share are full or read only).  q_out may be q
+ * with equal strides.  Inputs finite; others give unspecified codes in
+ * their own block and head.
+ */
+typedef struct {
+    const convrot_kv8_t *cache;
+    convrot_kv8_seqs_t seqs;
+    int32_t q_heads;
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    const void *k;
+    int64_t k_token_stride, k_head_stride;
+    const void *v;
+    int64_t v_token_stride, v_head_stride;
+    void *q_out;
+    int64_t q_out_token_stride, q_out_head_stride;
+    const void *q_weight, *k_weight;
+    float eps;
+    const convrot_rope_t *rope;
+    const int32_t *positions;
+} convrot_kv8_append_t;
+convrot_status_t convrot_kv8_append(const convrot_kv8_append_t *job, void *stream);
+
+/*
+ * Cached tokens back as BF16: row cu[b] + i of k_out and v_out [tokens,
+ * kv_heads, head_dim] (contiguous; one of them may be NULL) is the token at
+ * kv_len[b] - n + i of sequence b, bf16_rne(fl(code * scale)).
+ */
+typedef struct {
+    const convrot_kv8_t *cache;
+    convrot_kv8_seqs_t seqs;
+    void *k_out, *v_out;
+} convrot_kv8_read_t;
+convrot_status_t convrot_kv8_read(const convrot_kv8_read_t *job, void *stream);
+
+/*
+ * Attention of a step's queries over the cache:
+ *   out[t, h] = bf16_rne( sum_j softmax_j(scale * q[t, h] . K_j) V_j )
+ *   lse[t, h] = log sum_j exp(scale * q[t, h] . K_j)    (natural, fp32, or NULL)
+ * with K_j, V_j the cached values (code * scale) of the row's sequence at key
+ * head h / (q_heads / kv_heads), j up to the row's own position (causal 1) or
+ * over all kv_len tokens (causal 0).  A row that sees nothing gets zeros and
+ * lse = -infinity.  Any number of rows in a sequence, from single tokens to
+ * whole prompts, also mixed in one call.
+ *   q : [tokens, q_heads, head_dim], q_heads a multiple of kv_heads, <= 4096
+ *   out : BF16 [tokens, q_heads, head_dim] contiguous, overlaps no input
+ *   scale : > 0, finite
+ * Sums, maxima and accumulators are FP32; the weights of the value product
+ * are FP16 (11 bits).  A non-finite query gives NaN in its own row only.
+ * Results do not depend on the order in which the GPU runs the work.
+ * Workspace: convrot_attn_kv8_workspace_bytes (0 if the job is invalid),
+ * zero-filled before first use, left zero-filled where it has to be.
+ */
+typedef struct {
+    const convrot_kv8_t *cache;
+    convrot_kv8_seqs_t seqs;
+    int32_t q_heads, causal;
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    void *out;
+    float *lse;
+    float scale;
+} convrot_attn_kv8_t;
+convrot_status_t convrot_attn_kv8(const convrot_attn_kv8_t *job, void *ws, size_t ws_bytes, void *stream);
+size_t convrot_attn_kv8_workspace_bytes(const convrot_attn_kv8_t *job);
+
+/*
  * Synchronise `stream`, then read and clear the device-side status word of
  * the current device.  Returns CONVROT_OK, CONVROT_ERR_DEVICE_TIMEOUT if a
  * bounded wait ran out in some kernel since the last call (the workspace
  * must then be re-initialised), CONVROT_ERR_INVALID_ARG if a lookup met a
- * token outside its table, CONVROT_WARN_INEXACT_DOMAIN if a rotation met an
+ * token outside its table or a cache or rotation call an argument on the
+ * device that it could not use, CONVROT_WARN_INEXACT_DOMAIN if a rotation met an
  * input row that may lie outside the exact-sum domain (the results were
  * written; their low bits may differ from the exact-sum definition), or
  * CONVROT_ERR_CUDA.  A timeout overrides an earlier warning; the first

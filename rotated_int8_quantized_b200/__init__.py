@@ -14,6 +14,7 @@ Typical use::
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -90,6 +91,58 @@ class convrot_gemm_job_t(ctypes.Structure):
                 ("y_bf16", ctypes.c_void_p), ("acc", ctypes.c_void_p), ("bias_bf16", ctypes.c_void_p)]
 
 
+class convrot_kv8_t(ctypes.Structure):
+    """Mirror of the C struct: a view of a paged INT8 key/value cache."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k", "v", "k_scale", "v_scale")] + [("pages", ctypes.c_int64)] + \
+               [(f, ctypes.c_int32) for f in ("kv_heads", "page_tokens", "head_dim")]
+
+
+class convrot_rope_t(ctypes.Structure):
+    """Mirror of the C struct: the position rotation."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("axis", ctypes.c_void_p), ("axes", ctypes.c_int32)]
+
+
+class convrot_kv8_seqs_t(ctypes.Structure):
+    """Mirror of the C struct: the sequences of a step."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("page_table", "kv_len", "cu")] + [("tokens", ctypes.c_int64)] + \
+               [(f, ctypes.c_int32) for f in ("batch", "max_pages")]
+
+
+def _rows_fields(*names):
+    return [f for n in names for f in ((n, ctypes.c_void_p), (n + "_token_stride", ctypes.c_int64),
+                                       (n + "_head_stride", ctypes.c_int64))]
+
+
+_NORM_FIELDS = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rope", ctypes.POINTER(convrot_rope_t)), ("positions", ctypes.c_void_p)]
+
+
+class convrot_qk_norm_rope_t(ctypes.Structure):
+    """Mirror of the C struct: one convrot_qk_norm_rope call."""
+    _fields_ = [("tokens", ctypes.c_int64)] + [(f, ctypes.c_int32) for f in ("q_heads", "kv_heads", "head_dim")] + \
+        _rows_fields("q", "k", "q_out", "k_out") + _NORM_FIELDS
+
+
+class convrot_kv8_append_t(ctypes.Structure):
+    """Mirror of the C struct: one convrot_kv8_append call."""
+    _fields_ = [("cache", ctypes.POINTER(convrot_kv8_t)), ("seqs", convrot_kv8_seqs_t), ("q_heads", ctypes.c_int32)] + \
+        _rows_fields("q", "k", "v", "q_out") + _NORM_FIELDS
+
+
+class convrot_kv8_read_t(ctypes.Structure):
+    """Mirror of the C struct: one convrot_kv8_read call."""
+    _fields_ = [("cache", ctypes.POINTER(convrot_kv8_t)), ("seqs", convrot_kv8_seqs_t), ("k_out", ctypes.c_void_p),
+                ("v_out", ctypes.c_void_p)]
+
+
+class convrot_attn_kv8_t(ctypes.Structure):
+    """Mirror of the C struct: one convrot_attn_kv8 call."""
+    _fields_ = [("cache", ctypes.POINTER(convrot_kv8_t)), ("seqs", convrot_kv8_seqs_t), ("q_heads", ctypes.c_int32),
+                ("causal", ctypes.c_int32)] + _rows_fields("q") + \
+               [("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
 # exported symbol -> (argtypes, restype); every name declared in convrot.h
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _WP = ctypes.POINTER(convrot_weight_t)
@@ -126,6 +179,12 @@ SIGNATURES = {
     "convrot_gemm_i8_batch": ([_I64, ctypes.c_int, ctypes.POINTER(convrot_gemm_job_t), _P, _SZ, _P], ctypes.c_int),
     "convrot_gemm_batch_workspace_bytes": ([_I64, ctypes.c_int, ctypes.POINTER(convrot_gemm_job_t)], _SZ),
     "convrot_gemm_i8_noalloc": ([_P, _P, _I64, _WP, _P, _P, _P], ctypes.c_int),
+    "convrot_kv8_init": ([_P, _P, _P, _P, _P, _I64, _I32, _I32, _I32], ctypes.c_int),
+    "convrot_qk_norm_rope": ([_P, _P], ctypes.c_int),
+    "convrot_kv8_append": ([_P, _P], ctypes.c_int),
+    "convrot_kv8_read": ([_P, _P], ctypes.c_int),
+    "convrot_attn_kv8": ([_P, _P, _SZ, _P], ctypes.c_int),
+    "convrot_attn_kv8_workspace_bytes": ([_P], _SZ),
 }
 
 _lib = None
@@ -479,6 +538,274 @@ def conv2d_int8(x_nhwc: torch.Tensor, w: QuantizedWeight, kh: int, kw: int, stri
     _check(lib.convrot_conv2d_int8(_ptr(x_nhwc), ctypes.byref(g), ctypes.byref(w.handle), _ptr(y), _ptr(ws),
                                    ws.numel(), _stream(stream)), "convrot_conv2d_int8")
     return y
+
+
+# ---------------------------------------------------------------- attention beside the linears
+def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """FP32 [positions, rot_dim / 2, 2] cosines and sines of position *
+    theta^(-2 i / rot_dim), the angles taken in 64 bits."""
+    inv = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    angle = torch.arange(positions, dtype=torch.float64)[:, None] * inv
+    return torch.stack([angle.cos(), angle.sin()], -1).float().to(device)
+
+
+@dataclass
+class Rope:
+    """The position rotation: cos_sin fp32 [positions, rot_dim / 2, 2]
+    (rope_table), adjacent pairs (2 i, 2 i + 1) or pairs (i, i + rot_dim / 2),
+    and for several position axes a uint8 [rot_dim / 2] naming each pair's."""
+    cos_sin: torch.Tensor
+    adjacent: bool = False
+    axis: Optional[torch.Tensor] = None
+
+
+class KV8Cache:
+    """A paged INT8 key/value cache over caller-owned tensors: k, v int8
+    [pages, kv_heads, page_tokens, head_dim]; k_scale, v_scale fp32
+    [pages, kv_heads, page_tokens / 16]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        pages, heads, page, dim = k.shape
+        scales = (pages, heads, page // 16)
+        if v.shape != k.shape or tuple(k_scale.shape) != scales or tuple(v_scale.shape) != scales:
+            raise ValueError("expected codes [pages, kv_heads, page_tokens, head_dim] and scales "
+                             "[pages, kv_heads, page_tokens / 16]")
+        _want(torch.int8, k=k, v=v)
+        _want(torch.float32, k_scale=k_scale, v_scale=v_scale)
+        _one_device(k, v, k_scale, v_scale)
+        self.handle = convrot_kv8_t()
+        _check(load_library().convrot_kv8_init(ctypes.byref(self.handle), _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale),
+                                               pages, heads, page, dim), "convrot_kv8_init")
+
+
+def make_kv8_cache(pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> KV8Cache:
+    """Allocate a cache (nothing in it is read before a call has stored it)."""
+    codes = [torch.empty((pages, kv_heads, page_tokens, head_dim), dtype=torch.int8, device=device) for _ in "kv"]
+    scales = [torch.empty((pages, kv_heads, page_tokens // 16), dtype=torch.float32, device=device) for _ in "kv"]
+    return KV8Cache(*codes, *scales)
+
+
+def _want(dtype, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+
+
+def _one_device(*tensors) -> torch.device:
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("tensors on several devices: %s" % sorted(map(str, devices)))
+    return devices.pop()
+
+
+def _set_rows(job, name: str, t: Optional[torch.Tensor], heads: int, dim: int, tokens: int) -> None:
+    """A [tokens, heads, dim] BF16 view into a job's pointer and strides."""
+    if t is None:
+        return
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError("%s: expected BF16 [%d, %d, %d], got %s %s" % (name, tokens, heads, dim, t.dtype, tuple(t.shape)))
+    if not t.is_cuda or t.stride(2) != 1:
+        raise ValueError("%s: expected a CUDA tensor whose rows are contiguous" % name)
+    setattr(job, name, t.data_ptr())
+    setattr(job, name + "_token_stride", t.stride(0))
+    setattr(job, name + "_head_stride", t.stride(1))
+
+
+def _set_seqs(s: convrot_kv8_seqs_t, tokens: int, table: torch.Tensor, kv_len: torch.Tensor,
+              cu: Optional[torch.Tensor]) -> None:
+    _want(torch.int32, page_table=table, kv_len=kv_len, cu=cu)
+    if table.dim() != 2 or tuple(kv_len.shape) != (table.shape[0],) or \
+            (cu is not None and tuple(cu.shape) != (table.shape[0] + 1,)):
+        raise ValueError("expected page_table [batch, max_pages], kv_len [batch] and cu [batch + 1]")
+    s.page_table, s.kv_len, s.cu = _ptr(table), _ptr(kv_len), _ptr(cu)
+    s.tokens, s.batch, s.max_pages = tokens, table.shape[0], table.shape[1]
+
+
+def _set_norm(job, dim, tokens, q_weight, k_weight, eps, rope: Optional[Rope], positions) -> list:
+    """Fills in weights and rotation; returns what has to stay alive."""
+    _want(torch.bfloat16, q_weight=q_weight, k_weight=k_weight)
+    for w in (q_weight, k_weight):
+        if w is not None and tuple(w.shape) != (dim,):
+            raise ValueError("expected norm weights [%d], got %s" % (dim, tuple(w.shape)))
+    job.q_weight, job.k_weight, job.eps = _ptr(q_weight), _ptr(k_weight), eps
+    if rope is None:
+        return [q_weight, k_weight]
+    table, axes = rope.cos_sin, 1
+    _want(torch.float32, cos_sin=table)
+    _want(torch.uint8, axis=rope.axis)
+    if table.dim() != 3 or table.shape[2] != 2 or (rope.axis is not None and tuple(rope.axis.shape) != (table.shape[1],)):
+        raise ValueError("expected cos_sin [positions, rot_dim / 2, 2] and axis [rot_dim / 2]")
+    if positions is not None:
+        _want(torch.int32, positions=positions)
+        if positions.shape[-1] != tokens or positions.dim() not in (1, 2):
+            raise ValueError("expected positions [tokens] or [axes, tokens]")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+    r = convrot_rope_t(_ptr(table), table.shape[0], 2 * table.shape[1], 1 if rope.adjacent else 0, _ptr(rope.axis), axes)
+    job.rope, job.positions = ctypes.pointer(r), _ptr(positions)
+    return [q_weight, k_weight, rope, positions, r]
+
+
+class _Prepared:
+    """A prepared call: its C struct is built once, a step costs one C call
+    on the tensors' own device.  The tensors stay the caller's: new values
+    in them are what the next call works on."""
+    _entry = ""
+
+    def _args(self):
+        return (ctypes.byref(self.job),)
+
+    def __call__(self, stream=None) -> None:
+        fn = getattr(load_library(), self._entry)
+        if torch.cuda.current_device() == self.device.index:
+            status = fn(*self._args(), _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*self._args(), _stream(stream))
+        _check(status, self._entry)
+
+
+class QKNormRope(_Prepared):
+    """Norm and rotation of q [tokens, q_heads, head_dim] and (or None) k
+    [tokens, kv_heads, head_dim] into q_out, k_out (they may be q and k)."""
+    _entry = "convrot_qk_norm_rope"
+
+    def __init__(self, q, k, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6, rope: Optional[Rope] = None,
+                 positions=None):
+        tokens, heads, dim = q.shape
+        j = self.job = convrot_qk_norm_rope_t()
+        j.tokens, j.q_heads, j.kv_heads, j.head_dim = tokens, heads, 0 if k is None else k.shape[1], dim
+        for name, t, h in (("q", q, heads), ("k", k, j.kv_heads), ("q_out", q_out, heads), ("k_out", k_out, j.kv_heads)):
+            _set_rows(j, name, t, h, dim, tokens)
+        self.keep = [q, k, q_out, k_out, _set_norm(j, dim, tokens, q_weight, k_weight, eps, rope, positions)]
+        self.device = _one_device(q, k, q_out, k_out, q_weight, k_weight, positions,
+                                  *([rope.cos_sin, rope.axis] if rope else []))
+
+
+class KV8Append(_Prepared):
+    """Append a step's k, v [tokens, kv_heads, head_dim] to the cache, k
+    normalised and rotated, and put q (or None), normalised and rotated,
+    into q_out.  kv_len counts the new tokens; cu None: one per sequence;
+    positions None: the position in the sequence."""
+    _entry = "convrot_kv8_append"
+
+    def __init__(self, q, k, v, cache: KV8Cache, page_table, kv_len, q_out=None, cu=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, rope: Optional[Rope] = None, positions=None):
+        h = cache.handle
+        tokens = k.shape[0]
+        j = self.job = convrot_kv8_append_t()
+        j.cache, j.q_heads = ctypes.pointer(h), 0 if q is None else q.shape[1]
+        _set_seqs(j.seqs, tokens, page_table, kv_len, cu)
+        for name, t, n in (("q", q, j.q_heads), ("k", k, h.kv_heads), ("v", v, h.kv_heads), ("q_out", q_out, j.q_heads)):
+            _set_rows(j, name, t, n, h.head_dim, tokens)
+        self.keep = [q, k, v, q_out, cache, page_table, kv_len, cu,
+                     _set_norm(j, h.head_dim, tokens, q_weight, k_weight, eps, rope, positions)]
+        self.device = _one_device(q, k, v, q_out, cache.k, page_table, kv_len, cu, q_weight, k_weight, positions,
+                                  *([rope.cos_sin, rope.axis] if rope else []))
+
+
+class KV8Read(_Prepared):
+    """The last cu[b + 1] - cu[b] cached tokens of every sequence as BF16
+    rows of k_out and v_out [tokens, kv_heads, head_dim] (one may be None)."""
+    _entry = "convrot_kv8_read"
+
+    def __init__(self, cache: KV8Cache, page_table, kv_len, k_out, v_out, cu=None):
+        h = cache.handle
+        tokens = (k_out if k_out is not None else v_out).shape[0]
+        j = self.job = convrot_kv8_read_t()
+        j.cache = ctypes.pointer(h)
+        _set_seqs(j.seqs, tokens, page_table, kv_len, cu)
+        for t in (k_out, v_out):
+            if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, h.kv_heads, h.head_dim)):
+                raise ValueError("expected BF16 outputs [%d, %d, %d]" % (tokens, h.kv_heads, h.head_dim))
+        j.k_out, j.v_out = _ptr(k_out), _ptr(v_out)
+        self.keep = [cache, page_table, kv_len, k_out, v_out, cu]
+        self.device = _one_device(cache.k, page_table, kv_len, k_out, v_out, cu)
+
+
+class AttnKV8(_Prepared):
+    """Attention of q [tokens, q_heads, head_dim] over the cache into out
+    (contiguous, BF16) and, if given, lse [tokens, q_heads] (fp32).  The
+    rows of sequence b are its last cu[b + 1] - cu[b] tokens.  ws: a
+    zero-filled workspace of at least `ws_bytes`, which calls that run at the
+    same time must not share (allocated here if None)."""
+    _entry = "convrot_attn_kv8"
+
+    def __init__(self, q, cache: KV8Cache, page_table, kv_len, out, cu=None, lse=None, scale: Optional[float] = None,
+                 causal: bool = True, ws: Optional[torch.Tensor] = None):
+        h = cache.handle
+        tokens, heads, dim = q.shape
+        j = self.job = convrot_attn_kv8_t()
+        j.cache, j.q_heads, j.causal = ctypes.pointer(h), heads, 1 if causal else 0
+        j.scale = dim ** -0.5 if scale is None else scale
+        _set_seqs(j.seqs, tokens, page_table, kv_len, cu)
+        _set_rows(j, "q", q, heads, h.head_dim, tokens)
+        if out.dtype != torch.bfloat16 or tuple(out.shape) != tuple(q.shape):
+            raise ValueError("out: expected BF16 %s" % (tuple(q.shape),))
+        _want(torch.float32, lse=lse)
+        if lse is not None and tuple(lse.shape) != (tokens, heads):
+            raise ValueError("lse: expected [%d, %d]" % (tokens, heads))
+        j.out, j.lse = _ptr(out), _ptr(lse)
+        self.device = _one_device(q, cache.k, page_table, kv_len, out, cu, lse, ws)
+        with torch.cuda.device(self.device):
+            self.ws_bytes = int(load_library().convrot_attn_kv8_workspace_bytes(ctypes.byref(j)))
+        if ws is None:
+            # an invalid job needs none: the call says what is wrong with it
+            ws = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        self.ws = ws
+        self.keep = [q, cache, page_table, kv_len, out, cu, lse]
+
+    def _args(self):
+        return ctypes.byref(self.job), _ptr(self.ws), self.ws.numel() * self.ws.element_size()
+
+
+def _allocating(stream, device):
+    """Where the functions below make their tensors: on the stream they
+    launch on, so that fills and frees are ordered with the kernels."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
+    return torch.cuda.stream(stream)
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, rope: Optional[Rope] = None, positions=None,
+                 stream=None):
+    """QKNormRope into new tensors; returns (q_out, k_out)."""
+    with _allocating(stream, q.device):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    QKNormRope(q, k, q_out, k_out, q_weight, k_weight, eps, rope, positions)(stream)
+    return q_out, k_out
+
+
+def kv8_append(q, k, v, cache: KV8Cache, page_table, kv_len, cu=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+               rope: Optional[Rope] = None, positions=None, stream=None):
+    """KV8Append with a new q_out, which it returns (None without q)."""
+    with _allocating(stream, k.device):
+        q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    KV8Append(q, k, v, cache, page_table, kv_len, q_out, cu, q_weight, k_weight, eps, rope, positions)(stream)
+    return q_out
+
+
+def kv8_read(cache: KV8Cache, page_table, kv_len, tokens: Optional[int] = None, cu=None, stream=None):
+    """KV8Read into new tensors of `tokens` rows (batch rows without cu)."""
+    shape = (tokens if cu is not None else page_table.shape[0], cache.handle.kv_heads, cache.handle.head_dim)
+    with _allocating(stream, cache.k.device):
+        k, v = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) for _ in "kv")
+    KV8Read(cache, page_table, kv_len, k, v, cu)(stream)
+    return k, v
+
+
+def attn_kv8(q, cache: KV8Cache, page_table, kv_len, cu=None, scale: Optional[float] = None, causal: bool = True, ws=None,
+             stream=None):
+    """AttnKV8 into new tensors; returns (out, lse)."""
+    with _allocating(stream, q.device):
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+        call = AttnKV8(q, cache, page_table, kv_len, out, cu, lse, scale, causal, ws)
+    call(stream)
+    return out, lse
 
 
 def convrot_device_status(stream=None) -> None:

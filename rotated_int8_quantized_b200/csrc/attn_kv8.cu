@@ -1,0 +1,557 @@
+// attn_kv8.cu -- attention of a step's queries over the paged INT8 cache.
+//
+//   s_ij = scale * q_i . (ks_j kq_j)      keys' codes kq, one scale a block
+//   o_i  = sum_j softmax_j(s_ij) (vs_j vq_j)
+//
+// The codes are never dequantised one by one.  A code is exact in FP16, so
+// the products run on codes: a key block's scale multiplies 16 columns of
+// q . kq at once, and a value block's scale joins the exponent,
+//   p'_ij = exp2(s_ij log2(e) + log2(vs_j) - m_i),   o_i = sum_j p'_ij vq_j / l_i,   l_i = sum_j p'_ij / vs_j,
+// with m_i a running maximum of the exponents.  Queries become FP16 with a
+// power of two per row that brings the row's largest element to [2^14, 2^15):
+// exact for every element above 2^-28 of the largest, off by 2^-39 of the
+// largest below that (a BF16 product would be no closer).  p' is held as FP16
+// scaled by 2^7: 11 bits where BF16 keeps 8, and nothing above 2^-31 of the
+// row's running maximum (whose excess over the true one is at most 2^8) is
+// lost.  Sums, maxima and accumulators are FP32.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kv8.h"
+
+namespace convrot {
+
+constexpr int kStreamWarps = 4;
+constexpr int kStreamUnit = 16 * kStreamWarps;      // tokens a CTA takes at a time: a block for each warp
+constexpr float kPBias = 7.f;                       // p' is held times 2^7
+constexpr float kLazy = 8.f;                        // the running maximum moves once it is exceeded by 2^8
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Value scales below this count as this (a block of zeros has scale 0); the
+// values it stands for are below 2^-93.
+constexpr float kLeastScale = 7.888609052210118e-31f;   // 2^-100
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four codes to FP16 pairs: code + 128 is the low byte of the FP16 number
+// 1024 + (code + 128), from which 1152 is taken; every step is exact.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __half2half2(__ushort_as_half((unsigned short)0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), k), y = __hsub2(*reinterpret_cast<const __half2 *>(&b), k);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// d[16 x 8] += a[16 x 16] b[16 x 8], FP16 in, FP32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ld_stream16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_stream8(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// Rows, cached tokens and first row of sequence b, held to the step's bounds
+// whatever the device arrays say.
+struct SeqInfo {
+    int64_t t0;
+    int n, len;
+    bool bad;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const KvSeqs &s, int b) {
+    SeqInfo q;
+    int64_t t0 = b, t1 = b + 1;
+    if (s.cu) {
+        t0 = __ldg(s.cu + b);
+        t1 = __ldg(s.cu + b + 1);
+    }
+    const int64_t len = __ldg(s.kv_len + b), cap = (int64_t)s.max_pages << s.page_shift;
+    q.bad = t0 < 0 || t1 < t0 || t1 > s.tokens || len < 0 || len > cap;
+    t0 = min(max(t0, (int64_t)0), s.tokens);
+    t1 = min(max(t1, t0), s.tokens);
+    q.t0 = t0;
+    q.n = (int)(t1 - t0);
+    q.len = (int)min(max(len, (int64_t)0), cap);
+    return q;
+}
+
+// ------------------------------------------------------------ few rows a sequence
+//
+// The queries of one sequence that share a key head are the rows of a tile:
+// row r is token r / group, head kv_head * group + r % group.  A CTA of four
+// warps streams the cache through such tiles of 8 NT rows; warp w takes block
+// w of every four blocks of 16 tokens, from global memory straight into the
+// operand layout of mma.m16n8k16 (16 tokens x 16 dims of K as the first
+// operand, 16 dims x 16 tokens of V; the sums run over dims, then tokens, in an
+// order of our choosing, so a lane simply takes 16 consecutive bytes of a row
+// and queries and outputs follow the same order).  The next block is in flight
+// while one is worked on.
+//
+// Bound by memory, so the cache's blocks are dealt out evenly: all units (64
+// tokens of a tile) of the step in one list, an equal range for each of the
+// resident CTAs, whatever the lengths.  A tile that a range cuts leaves its
+// parts (FP32 sums, maximum) in the workspace, and the CTA that finds itself
+// last at the tile's counter joins them, in the order of the ranges, and sets
+// the counter back to zero.
+template <int D, int NT>
+struct StreamSmem {
+    float o[kStreamWarps][8 * NT][D + 4];
+    float m[kStreamWarps][8 * NT], l[kStreamWarps][8 * NT];
+    long long first[kStreamWarps];
+    int seq, last;
+    long long seq_unit;
+};
+
+// CTAs of the persistent grid on an SM; also what the registers are held to.
+constexpr int stream_ctas(int nt) { return nt == 1 ? 3 : 2; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int R = 8 * NT, T = kStreamWarps * 32;
+    constexpr int CH = D / 64;                       // 16-byte chunks of a K row a lane holds
+    constexpr int VW = D / 32;                       // words of a V row a lane holds
+    constexpr int MT = D / 16;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    StreamSmem<D, NT> &sm = *reinterpret_cast<StreamSmem<D, NT> *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int H = a.c.heads, group = a.q_heads / H;
+    const KvSeqs &S = a.s;
+
+    // units of every sequence, summed; thread i holds sequences [i per, i per + per)
+    const int per = (S.batch + T - 1) / T;
+    auto seq_units = [&](const SeqInfo &q) {
+        const int tiles = (int)(((long long)q.n * group + R - 1) / R);
+        const int units = q.len > 0 ? (q.len + kStreamUnit - 1) / kStreamUnit : 1;   // empty rows are written too
+        return (long long)tiles * units * H;
+    };
+    long long mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= S.batch) break;
+        const SeqInfo q = seq_info(S, b);
+        if (q.bad && blockIdx.x == 0) report_invalid();
+        mine += seq_units(q);
+    }
+    long long scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) sm.first[warp] = scan;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kStreamWarps; ++w) {
+        const long long v = sm.first[w];
+        if (w < warp) before += v;
+        total += v;
+    }
+    before += scan - mine;
+    const long long G = min((long long)gridDim.x, total);
+    const long long c = blockIdx.x;
+    if (c >= G) return;
+    long long u = total * c / G;
+    const long long u1 = total * (c + 1) / G;
+    if (before <= u && u < before + mine) {
+        long long x = before;
+        int b = tid * per;
+        for (; b + 1 < S.batch; ++b) {
+            const long long n = seq_units(seq_info(S, b));
+            if (u < x + n) break;
+            x += n;
+        }
+        sm.seq = b;
+        sm.seq_unit = x;
+    }
+    __syncthreads();
+    int b = sm.seq;
+    long long seq_unit = sm.seq_unit;
+    SeqInfo q = seq_info(S, b);
+
+    int *const counters = static_cast<int *>(a.ws);
+    float *const parts = reinterpret_cast<float *>(counters + ((gridDim.x + 63) & ~63u));
+    constexpr int kPart = R * (D + 2);
+
+    while (u < u1) {
+        // the tile of unit u
+        long long n_units;
+        while (u >= seq_unit + (n_units = seq_units(q)) && b + 1 < S.batch) {
+            seq_unit += n_units;
+            ++b;
+            q = seq_info(S, b);
+        }
+        const int units = q.len > 0 ? (q.len + kStreamUnit - 1) / kStreamUnit : 1;
+        const int tiles = (int)(((long long)q.n * group + R - 1) / R);
+        if (tiles == 0) break;                       // only if the lengths changed under the kernel
+        const long long tile_index = (u - seq_unit) / units;
+        const long long tile_unit = seq_unit + tile_index * units;
+        const int h = (int)(tile_index / tiles), rt = (int)(tile_index - (long long)h * tiles);
+        const int unit0 = (int)(u - tile_unit);
+        const int unit1 = (int)min((long long)units, u1 - tile_unit);
+
+        // queries: row 8 nt + g, dims 64 ch + 16 t4 .. + 15
+        uint32_t qf[NT][CH][4][2];
+        float f[NT][2];                              // rows 8 nt + 2 t4, + 1: log2(e) * softmax scale * row scale
+        int vis[NT][2];                              // tokens they see
+        int most = 0, least = 0x7fffffff;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int64_t row = (int64_t)rt * R + 8 * nt + g;
+            const bool in = row < (int64_t)q.n * group;
+            const int64_t tok = row / group;
+            const int head = h * group + (int)(row - tok * group);
+            const uint16_t *src = a.q.p + (q.t0 + tok) * a.q.ts + (int64_t)head * a.q.hs;
+            float y[CH][16];
+            float top = 0.f;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+                if (in) {
+                    x[0] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * ch + 16 * t4));
+                    x[1] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * ch + 16 * t4) + 1);
+                }
+                const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[ch][2 * i] = __uint_as_float(w[i] << 16);
+                    y[ch][2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                    top = fmaxf(top, fmaxf(fabsf(y[ch][2 * i]), fabsf(y[ch][2 * i + 1])));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(14 - e), e the exponent of the row's largest element (held to what FP32 can scale by)
+            int e = (int)(__float_as_uint(top) >> 23) - 127;
+            e = e > 127 ? 0 : (e < -100 ? -100 : e);
+            const float up = __int_as_float((127 + 14 - e) << 23);
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        qf[nt][ch][i][k] = pack_half2(y[ch][4 * i + 2 * k] * up, y[ch][4 * i + 2 * k + 1] * up);
+            const float down = a.scale * kLog2e * __int_as_float((127 - 14 + e) << 23);
+            int64_t seen = !in ? 0 : (a.causal ? (int64_t)q.len - q.n + tok + 1 : q.len);
+            const int v = (int)max((int64_t)0, min(seen, (int64_t)q.len));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                f[nt][k] = __shfl_sync(0xffffffffu, down, (2 * t4 + k) * 4);
+                vis[nt][k] = __shfl_sync(0xffffffffu, v, (2 * t4 + k) * 4);
+            }
+            most = max(most, __reduce_max_sync(0xffffffffu, v));
+            least = min(least, __reduce_min_sync(0xffffffffu, v));
+        }
+
+        float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+
+        // this warp's blocks: warp, warp + 4, .. of [4 unit0, 4 unit1), as far as a row sees
+        const int blk1 = min(unit1 * kStreamWarps, (most + 15) >> 4);
+        const int32_t *pages = S.table + (int64_t)b * S.max_pages;
+        const int bshift = S.page_shift - 4, bmask = (1 << bshift) - 1;
+        uint4 kr[2][2][CH];
+        uint32_t vr[2][4][VW];
+        float ks[2], vs[2];
+        auto page_of = [&](int blk) { return blk < blk1 ? __ldg(pages + (blk >> bshift)) : 0; };
+        auto load = [&](int blk, int page, int buf) {
+            if (blk >= blk1) return;
+            const bool ok = page >= 0 && page < S.pages;
+            if (!ok) {                               // no such page: its tokens are not seen
+                if (lane == 0) report_invalid();
+                ks[buf] = -1.f;
+                return;
+            }
+            const int64_t sc = (((int64_t)page * H + h) << bshift) + (blk & bmask);
+            ks[buf] = __ldg(a.c.ks + sc);
+            vs[buf] = __ldg(a.c.vs + sc);
+            const int8_t *kp = a.c.k + sc * (16 * D), *vp = a.c.v + sc * (16 * D);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) kr[buf][r][ch] = ld_stream16(kp + (g + 8 * r) * D + 64 * ch + 16 * t4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int8_t *p = vp + (2 * t4 + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
+                if constexpr (VW == 4) {
+                    const uint4 x = ld_stream16(p);
+                    vr[buf][r][0] = x.x, vr[buf][r][1] = x.y, vr[buf][r][2] = x.z, vr[buf][r][3] = x.w;
+                } else {
+                    const uint2 x = ld_stream8(p);
+                    vr[buf][r][0] = x.x, vr[buf][r][1] = x.y;
+                }
+            }
+        };
+        auto work = [&](int blk, int buf) {
+            if (blk >= blk1 || ks[buf] < 0.f) return;
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                const uint32_t w0[4] = {kr[buf][0][ch].x, kr[buf][0][ch].y, kr[buf][0][ch].z, kr[buf][0][ch].w};
+                const uint32_t w1[4] = {kr[buf][1][ch].x, kr[buf][1][ch].y, kr[buf][1][ch].z, kr[buf][1][ch].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_half(w0[i], a0, a2);
+                    codes_to_half(w1[i], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][ch][i][0], qf[nt][ch][i][1]);
+                }
+            }
+            const float ve = fmaxf(vs[buf], kLeastScale), lv = __log2f(ve), iv = __fdividef(1.f, ve);
+            const int at = blk * 16 + g;
+            const bool whole = blk * 16 + 16 <= least;
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s[nt][k] = fmaf(s[nt][k], f[nt][k & 1] * ks[buf], lv);
+                    if (!whole && at + 8 * (k >> 1) >= vis[nt][k & 1]) s[nt][k] = -INFINITY;
+                    over |= s[nt][k] > m[nt][k & 1] + kLazy;
+                }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float x = fmaxf(s[nt][k], s[nt][k + 2]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        // by this row alone: what a row gets does not depend on its neighbours
+                        const float mn = x > m[nt][k] + kLazy ? x : m[nt][k];
+                        const float al = m[nt][k] == mn ? 1.f : ex2(m[nt][k] - mn);
+                        m[nt][k] = mn;
+                        l[nt][k] *= al;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) o[nt][i][k] *= al, o[nt][i][k + 2] *= al;
+                    }
+            }
+            uint32_t p0[NT], p1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float mm = m[nt][k & 1] == -INFINITY ? 0.f : m[nt][k & 1];
+                    p[k] = ex2(s[nt][k] - mm + kPBias);
+                }
+                l[nt][0] = fmaf(p[0] + p[2], iv, l[nt][0]);
+                l[nt][1] = fmaf(p[1] + p[3], iv, l[nt][1]);
+                p0[nt] = movmatrix_trans(pack_half2(p[0], p[1]));
+                p1[nt] = movmatrix_trans(pack_half2(p[2], p[3]));
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                // bytes of tokens (2 t4, 2 t4 + 1) and (2 t4 + 8, 2 t4 + 9) side by side, dims 4 w .. 4 w + 3
+                uint32_t x[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t lo = __byte_perm(vr[buf][2 * k][w], vr[buf][2 * k + 1][w], 0x5140);
+                    const uint32_t hi = __byte_perm(vr[buf][2 * k][w], vr[buf][2 * k + 1][w], 0x7362);
+                    codes_to_half(lo, x[k][0], x[k][1]);
+                    codes_to_half(hi, x[k][2], x[k][3]);
+                }
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(o[nt][2 * w + d], x[0][2 * d], x[0][2 * d + 1], x[1][2 * d], x[1][2 * d + 1], p0[nt], p1[nt]);
+            }
+        };
+        {
+            int blk = unit0 * kStreamWarps + warp;
+            int page = page_of(blk), next = page_of(blk + kStreamWarps);
+            load(blk, page, 0);
+            while (blk < blk1) {
+                page = next;
+                next = page_of(blk + 2 * kStreamWarps);
+                load(blk + kStreamWarps, page, 1);
+                work(blk, 0);
+                blk += kStreamWarps;
+                page = next;
+                next = page_of(blk + 2 * kStreamWarps);
+                load(blk + kStreamWarps, page, 0);
+                work(blk, 1);
+                blk += kStreamWarps;
+            }
+        }
+
+        // the four warps' parts
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x = l[nt][k];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                const int r = 8 * nt + 2 * t4 + k;
+                if (g == 0) sm.m[warp][r] = m[nt][k], sm.l[warp][r] = x;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    // fragment rows g and g + 8 of tile i are dims (D / 8) g + 2 i and + 1
+                    *reinterpret_cast<float2 *>(&sm.o[warp][r][(D / 8) * g + 2 * i]) = make_float2(o[nt][i][k], o[nt][i][k + 2]);
+                }
+            }
+        __syncthreads();
+        const bool cut = unit0 > 0 || unit1 < units;
+        float *part = parts + ((long long)(2 * c) + (u == total * c / G ? 0 : 1)) * kPart;
+        constexpr int PER = R * D / T;               // outputs of a thread, consecutive dims of one row
+        const int r = tid * PER / D, d0 = tid * PER % D;
+        auto write_out = [&](const float (&x)[PER], float M, float L) {
+            const int64_t row = (int64_t)rt * R + r;
+            if (row >= (int64_t)q.n * group) return;
+            const int64_t tok = row / group;
+            const int64_t at = (q.t0 + tok) * a.q_heads + h * group + (row - tok * group);
+            const float inv = L == 0.f ? 0.f : 1.f / L;             // nothing seen: zeros
+            uint32_t w[PER / 2];
+#pragma unroll
+            for (int i = 0; i < PER / 2; ++i) w[i] = pack_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+            uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * D + d0);
+#pragma unroll
+            for (int i = 0; i < PER / 2; ++i) dst[i] = w[i];
+            if (a.lse && d0 == 0) a.lse[at] = L == 0.f ? -INFINITY : (M - kPBias + log2f(L)) * kLn2;
+        };
+        {
+            float M = -INFINITY, L = 0.f, x[PER], wt[kStreamWarps];
+#pragma unroll
+            for (int w = 0; w < kStreamWarps; ++w) M = fmaxf(M, sm.m[w][r]);
+#pragma unroll
+            for (int w = 0; w < kStreamWarps; ++w) {
+                wt[w] = sm.m[w][r] == -INFINITY ? (sm.l[w][r] != sm.l[w][r] ? sm.l[w][r] : 0.f) : ex2(sm.m[w][r] - M);
+                L = fmaf(wt[w], sm.l[w][r], L);
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                x[i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kStreamWarps; ++w) x[i] = fmaf(wt[w], sm.o[w][r][d0 + i], x[i]);
+            }
+            if (!cut) {
+                write_out(x, M, L);
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) __stcg(part + r * D + d0 + i, x[i]);
+                if (d0 == 0) {
+                    __stcg(part + R * D + 2 * r, M);
+                    __stcg(part + R * D + 2 * r + 1, L);
+                }
+            }
+        }
+        if (cut) {
+            __threadfence();
+            __syncthreads();
+            // ranges c0 .. c1 hold the tile; range c starts at total * c / G
+            auto range_of = [&](long long unit) {
+                long long x = unit * G / total;
+                while (x + 1 < G && total * (x + 1) / G <= unit) ++x;
+                while (x > 0 && total * x / G > unit) --x;
+                return x;
+            };
+            const long long c0 = range_of(tile_unit), c1 = range_of(tile_unit + units - 1);
+            if (tid == 0) {
+                const int seen = atomicAdd(counters + c0, 1);
+                sm.last = seen == (int)(c1 - c0);
+                if (sm.last) counters[c0] = 0;
+            }
+            __syncthreads();
+            if (sm.last) {
+                __threadfence();
+                float M = -INFINITY, L = 0.f, x[PER];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) x[i] = 0.f;
+                for (long long cc = c0; cc <= c1; ++cc) {
+                    const float *p = parts + (2 * cc + (cc == c0 && total * c0 / G != tile_unit ? 1 : 0)) * kPart;
+                    const float pm = __ldcg(p + R * D + 2 * r), pl = __ldcg(p + R * D + 2 * r + 1);
+                    if (pm == -INFINITY && pl == 0.f) continue;
+                    const float mn = fmaxf(M, pm);
+                    const float wa = M == -INFINITY ? 0.f : ex2(M - mn), wb = pm == -INFINITY ? pl : ex2(pm - mn);
+                    L = L * wa + pl * wb;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) x[i] = x[i] * wa + __ldcg(p + r * D + d0 + i) * wb;
+                    M = mn;
+                }
+                write_out(x, M, L);
+            }
+        }
+        u = tile_unit + unit1;
+    }
+}
+
+// Rows of a tile: 8 where a sequence has no more, 16 otherwise (the next tile of
+// the same head reads the cache again, mostly from L2).
+static int stream_tiles(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads) {
+    const int64_t rows = (tokens + batch - 1) / batch * (q_heads / kv_heads);
+    return rows <= 8 ? 1 : 2;
+}
+
+int64_t attn_kv8_workspace_bytes(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int sms) {
+    const int nt = stream_tiles(tokens, batch, q_heads, kv_heads);
+    const int64_t grid = (int64_t)sms * stream_ctas(nt), rows = 8 * nt;
+    return ((grid + 63) / 64 * 64 + 2 * grid * rows * (dim + 2)) * 4;
+}
+
+template <int D, int NT>
+static cudaError_t launch_stream(const AttnArgs &a, int sms, cudaStream_t stream) {
+    const int bytes = (int)sizeof(StreamSmem<D, NT>);
+    cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    attn_stream_kernel<D, NT><<<sms * stream_ctas(NT), kStreamWarps * 32, bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_kv8(const AttnArgs &a, int sms, cudaStream_t stream) {
+    const int nt = stream_tiles(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
+    if (a.c.dim == 128) return nt == 1 ? launch_stream<128, 1>(a, sms, stream) : launch_stream<128, 2>(a, sms, stream);
+    return nt == 1 ? launch_stream<64, 1>(a, sms, stream) : launch_stream<64, 2>(a, sms, stream);
+}
+
+}  // namespace convrot

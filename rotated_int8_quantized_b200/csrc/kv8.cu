@@ -1,0 +1,531 @@
+// kv8.cu -- what stands between the q/k/v projections and attention: norms
+// of queries and keys per head with the position rotation in the same pass,
+// and the paged INT8 key/value cache (append, read).
+//
+//   norm    y_d = x_d * rsqrt(mean_d(x_d^2) + eps) * w_d          per head
+//   rotate  (a, b) -> (a c - b s, b c + a s)      c, s = table[position][pair]
+//   store   codes q = clamp(rne(x / s), +-127), one FP32 scale s for every
+//           16 tokens of a page and head
+//
+// All of it is bound by memory: a value is loaded once as BF16, kept in
+// FP32 registers through norm and rotation, and rounded once on its way out
+// (to BF16, or to its INT8 code).
+//
+// A row (one head of one token) belongs to dim / 8 consecutive lanes, eight
+// values each.  With the pairs (i, i + rot / 2) a lane holds dims 4i .. 4i+3
+// and their partners, so the rotation needs no exchange between lanes and a
+// lane needs four table entries (32 bytes) for all the heads it works on.
+//
+// The scale of a block that still has room.  A block of 16 tokens is filled
+// by one call or, token by token, by sixteen.  Its first tokens set
+// s = max|x| / 127; later tokens keep s while they fit (max|x| < 127.5 s: no
+// code would round past 127), and double it as often as it takes when they do
+// not, the older codes q becoming rne(q / 2^j).  Doubling, not max|x| / 127
+// again, bounds what a value can lose to the block's history: roundings of
+// 0.5 s, 0.5 s / 2, 0.5 s / 4 .. in units of the final scale s, less than one
+// step in all however the tokens arrived, where rescaling to every new
+// maximum could round sixteen times at full size.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kv8.h"
+
+namespace convrot {
+
+constexpr int kHeadThreads = 256;
+
+// An invalid argument that only the device can see: recorded unless another
+// error is (a warning gives way).
+__device__ __forceinline__ void report_invalid() {
+    if (atomicCAS(&g_device_status, 0, 1 /* CONVROT_ERR_INVALID_ARG */) == 8) atomicCAS(&g_device_status, 8, 1);
+}
+
+// ------------------------------------------------------------ sequences
+// Token row t of a step belongs to sequence b with cu[b] <= t < cu[b + 1],
+// at cache position kv_len[b] - (cu[b + 1] - t).
+struct TokenPlace {
+    int b;                // -1: behind the last sequence
+    int64_t pos;          // < 0: padding, the sequence is shorter than its rows
+};
+
+// The last b in [0, batch) with key(b) <= x, for key monotone in b; -1 if
+// there is none.  L consecutive lanes search together, L probes a step.
+template <int L, typename Key>
+__device__ __forceinline__ int search_lanes(int batch, int64_t x, Key key) {
+    const int lane = threadIdx.x & (L - 1);
+    const unsigned group = (L == 32) ? 0xffffffffu : (((1u << (L & 31)) - 1u) << (threadIdx.x & 31 & ~(L - 1)));
+    int lo = 0, n = batch;
+    while (true) {
+        const int step = (n + L - 1) / L;
+        const int i = lo + lane * step;
+        const bool le = lane * step < n && key(i) <= x;
+        const int c = __popc(__ballot_sync(group, le) & group);
+        if (c == 0) return -1;
+        const int end = lo + n;
+        lo += (c - 1) * step;
+        if (step == 1) return lo;
+        n = end - lo < step ? end - lo : step;
+    }
+}
+
+template <int L>
+__device__ __forceinline__ TokenPlace place_token(const KvSeqs &s, int64_t t) {
+    TokenPlace p;
+    if (!s.cu) {
+        p.b = (int)t;
+        p.pos = (int64_t)__ldg(s.kv_len + t) - 1;
+        return p;
+    }
+    const int b = search_lanes<L>(s.batch, t, [&](int i) { return (int64_t)__ldg(s.cu + i); });
+    p.b = -1;
+    p.pos = -1;
+    if (b < 0) return p;
+    const int64_t end = __ldg(s.cu + b + 1);
+    if (t >= end) return p;
+    p.b = b;
+    p.pos = (int64_t)__ldg(s.kv_len + b) - (end - t);
+    return p;
+}
+
+// ------------------------------------------------------------ head rows
+// Where a lane's eight values lie in a row, and its rotation's coefficients.
+struct LaneGeo {
+    int a, b;             // dims a .. a+3 and b .. b+3
+    bool rotated;
+};
+
+__device__ __forceinline__ LaneGeo lane_geo(int lane, const RopeArgs &r) {
+    LaneGeo g;
+    const int rl = r.cs ? r.rot / 8 : 0;
+    g.rotated = lane < rl;
+    if (g.rotated && !r.adjacent) {
+        g.a = 4 * lane;
+        g.b = r.rot / 2 + 4 * lane;
+    } else {
+        g.a = 8 * lane;
+        g.b = 8 * lane + 4;
+    }
+    return g;
+}
+
+// Coefficients of pairs 4 lane .. 4 lane + 3 at token row t (cache position
+// `pos` where the caller gives no positions).  False if a position lies
+// outside the table or an axis outside the positions.
+__device__ __forceinline__ bool load_rotation(const RopeArgs &r, const LaneGeo &g, int lane, int64_t t, int64_t tokens,
+                                              int64_t pos, float (&c)[4], float (&s)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
+    if (!g.rotated) return true;
+    const int half = r.rot / 2;
+    if (!r.axis) {
+        const int64_t p = r.pos ? (int64_t)__ldg(r.pos + t) : pos;
+        if (p < 0 || p >= r.rows) return false;
+        const float4 *e = reinterpret_cast<const float4 *>(r.cs + (p * half + 4 * lane) * 2);
+        const float4 x = __ldg(e), y = __ldg(e + 1);
+        c[0] = x.x, s[0] = x.y, c[1] = x.z, s[1] = x.w;
+        c[2] = y.x, s[2] = y.y, c[3] = y.z, s[3] = y.w;
+        return true;
+    }
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int ax = __ldg(r.axis + 4 * lane + i);
+        const int64_t p = ax < r.axes ? (int64_t)__ldg(r.pos + ax * tokens + t) : -1;
+        if (p < 0 || p >= r.rows) {
+            ok = false;
+            continue;
+        }
+        const float2 e = __ldg(reinterpret_cast<const float2 *>(r.cs) + p * half + 4 * lane + i);
+        c[i] = e.x;
+        s[i] = e.y;
+    }
+    return ok;
+}
+
+__device__ __forceinline__ void unpack_bf16x4(const uint2 &w, float *y) {
+    y[0] = __uint_as_float(w.x << 16);
+    y[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    y[2] = __uint_as_float(w.y << 16);
+    y[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    __nv_bfloat162 h = __halves2bfloat162(__float2bfloat16_rn(lo), __float2bfloat16_rn(hi));
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Norm (if w) and rotation of a row's values, y[0..3] at g.a and y[4..7] at
+// g.b; the row's L lanes call it together.
+template <int L>
+__device__ __forceinline__ void norm_rotate(float (&y)[8], const float (&w)[8], bool norm, float eps, const LaneGeo &g,
+                                            bool adjacent, const float (&c)[4], const float (&s)[4]) {
+    if (norm) {
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q = fmaf(y[i], y[i], q);
+        // lanes of other rows of the warp may have left: only this row's take part
+        const unsigned group = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) q += __shfl_xor_sync(group, q, o);
+        const float r = rsqrtf(q * (1.f / (8 * L)) + eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+    }
+    if (!g.rotated) return;
+    if (adjacent) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = y[2 * i], v = y[2 * i + 1];
+            y[2 * i] = u * c[i] - v * s[i];
+            y[2 * i + 1] = v * c[i] + u * s[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = y[i], v = y[4 + i];
+            y[i] = u * c[i] - v * s[i];
+            y[4 + i] = v * c[i] + u * s[i];
+        }
+    }
+}
+
+__device__ __forceinline__ void load_weight(const uint16_t *w, const LaneGeo &g, float (&out)[8]) {
+    if (!w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = 1.f;
+        return;
+    }
+    unpack_bf16x4(__ldg(reinterpret_cast<const uint2 *>(w + g.a)), out);
+    unpack_bf16x4(__ldg(reinterpret_cast<const uint2 *>(w + g.b)), out + 4);
+}
+
+// Heads [h0, h1) of token row t: load, norm, rotate, round, store.  Rows may
+// be rotated in place, so plain loads.
+template <int L>
+__device__ __forceinline__ void head_rows(const HeadRows &in, const HeadRowsOut &out, int64_t t, int h0, int h1,
+                                          const uint16_t *weight, float eps, const LaneGeo &g, bool adjacent, bool zero,
+                                          const float (&c)[4], const float (&s)[4]) {
+    constexpr int U = 4;                  // rows in flight
+    float w[8];
+    load_weight(weight, g, w);
+    const uint16_t *src = in.p + t * in.ts;
+    uint16_t *dst = out.p + t * out.ts;
+    for (int h = h0; h < h1; h += U) {
+        uint2 x[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (h + u < h1) {
+                x[u][0] = *reinterpret_cast<const uint2 *>(src + (h + u) * in.hs + g.a);
+                x[u][1] = *reinterpret_cast<const uint2 *>(src + (h + u) * in.hs + g.b);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (h + u < h1) {
+                float y[8];
+                unpack_bf16x4(x[u][0], y);
+                unpack_bf16x4(x[u][1], y + 4);
+                norm_rotate<L>(y, w, weight != nullptr, eps, g, adjacent, c, s);
+                uint2 lo = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                uint2 hi = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                if (zero) lo = hi = make_uint2(0u, 0u);
+                *reinterpret_cast<uint2 *>(dst + (h + u) * out.hs + g.a) = lo;
+                *reinterpret_cast<uint2 *>(dst + (h + u) * out.hs + g.b) = hi;
+            }
+    }
+}
+
+template <int L>
+__device__ __forceinline__ bool all_lanes(bool ok) {
+    const unsigned group = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
+    return __all_sync(group, ok);
+}
+
+template <int L>
+__global__ void __launch_bounds__(kHeadThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per, int cq,
+                                                               int chunks) {
+    const int lane = threadIdx.x & (L - 1);
+    const int64_t task = (int64_t)blockIdx.x * (kHeadThreads / L) + threadIdx.x / L;
+    const int64_t t = task / chunks;
+    if (t >= a.tokens) return;
+    const int ch = (int)(task - t * chunks);
+    const LaneGeo g = lane_geo(lane, a.rope);
+    float c[4], s[4];
+    const bool ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.tokens, -1, c, s));
+    if (!ok && lane == 0) report_invalid();
+    if (ch < cq) {
+        const int h0 = ch * per;
+        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent, !ok, c, s);
+    } else {
+        const int h0 = (ch - cq) * per;
+        head_rows<L>(a.k, a.k_out, t, h0, min(h0 + per, a.kv_heads), a.kw, a.eps, g, a.rope.adjacent, !ok, c, s);
+    }
+}
+
+// Heads a lane group takes one after another: one while there are few rows
+// (latency), up to eight once the GPU is full (the table entries and weights
+// are then loaded once for eight heads).
+static int heads_per_group(int64_t tokens, int heads, int lanes, int sms) {
+    const int64_t groups = (int64_t)sms * 2048 / lanes;
+    int per = 1;
+    while (per < 8 && tokens * heads > groups * per * 2) per *= 2;
+    return per;
+}
+
+cudaError_t launch_norm_rope(const NormRopeArgs &a, int sms, cudaStream_t stream) {
+    const int L = a.dim / 8;
+    const int per = heads_per_group(a.tokens, a.q_heads + a.kv_heads, L, sms);
+    const int cq = (a.q_heads + per - 1) / per, chunks = cq + (a.kv_heads + per - 1) / per;
+    const int64_t blocks = (a.tokens * chunks + kHeadThreads / L - 1) / (kHeadThreads / L);
+    if (L == 16)
+        norm_rope_kernel<16><<<(unsigned)blocks, kHeadThreads, 0, stream>>>(a, per, cq, chunks);
+    else
+        norm_rope_kernel<8><<<(unsigned)blocks, kHeadThreads, 0, stream>>>(a, per, cq, chunks);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------ append
+// Codes of a lane's eight values on scale s (0: an all-zero block).
+__device__ __forceinline__ uint32_t codes4(const float *y, float s) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float q = s > 0.f ? rintf(__fdiv_rn(y[i], s)) : 0.f;
+        q = fminf(fmaxf(q, -127.f), 127.f);
+        w |= ((uint32_t)(int)q & 0xFFu) << (8 * i);
+    }
+    return w;
+}
+
+// rne(q * f) of four codes; f = 2^-j (or 0), so the product is exact.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float q = (float)(int8_t)(w >> (8 * i));
+        r |= ((uint32_t)(int)rintf(q * f) & 0xFFu) << (8 * i);
+    }
+    return r;
+}
+
+// The block's scale once values up to `most` join it.  held: the block has
+// older tokens, on scale old.  shrink: what their codes are multiplied by.
+__device__ __forceinline__ float grow_scale(float most, bool held, float old, float &shrink) {
+    shrink = 1.f;
+    if (!held) return __fdiv_rn(most, 127.f);
+    if (most == 0.f) return old;
+    const float r = __fdiv_rn(most, 127.5f * old);
+    if (!(old > 0.f) || !(r < 16777216.f)) {       // nothing of the older codes (all below half a step) is left
+        shrink = 0.f;
+        return __fdiv_rn(most, 127.f);
+    }
+    if (r < 1.f) return old;
+    const int j = ilogbf(r) + 1;
+    shrink = __int_as_float((127 - j) << 23);
+    return old * __int_as_float((127 + j) << 23);
+}
+
+// CTA = 16 rows x L lanes: one block of 16 tokens of one head, keys and
+// values together (blockIdx.x < kv_ctas), or chunks of the queries' heads.
+template <int L>
+__global__ void __launch_bounds__(16 * L) kv8_append_kernel(const __grid_constant__ AppendArgs a, int64_t kv_ctas, int per,
+                                                          int chunks) {
+    const int lane = threadIdx.x & (L - 1), row = threadIdx.x / L;
+    const LaneGeo g = lane_geo(lane, a.rope);
+    const int64_t cap = (int64_t)a.s.max_pages << a.s.page_shift;
+    float c[4], s[4];
+    if ((int64_t)blockIdx.x >= kv_ctas) {
+        // ---------------------------------------------------- queries
+        const int64_t task = ((int64_t)blockIdx.x - kv_ctas) * 16 + row;
+        const int64_t t = task / chunks;
+        if (t >= a.s.tokens) return;
+        const TokenPlace p = place_token<L>(a.s, t);
+        if (p.b < 0) return;
+        const bool pad = p.pos < 0;
+        bool ok = true;
+        if (!pad) ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.s.tokens, p.pos, c, s)) && p.pos < cap;
+        if (!ok && lane == 0) report_invalid();
+        const int h0 = (int)(task - t * chunks) * per;
+        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent, pad || !ok, c, s);
+        return;
+    }
+    // -------------------------------------------------------- keys, values
+    __shared__ float most_k[16], most_v[16];
+    const int H = a.c.heads;
+    const int64_t slot = blockIdx.x / H;
+    const int h = (int)(blockIdx.x - slot * H);
+    // sequence b owns the block slots from cu[b] / 16 + 2 b on: enough for
+    // its n tokens wherever they start in a block
+    int b;
+    int64_t t0, n, j;
+    if (!a.s.cu) {
+        b = (int)slot;
+        t0 = slot;
+        n = 1;
+        j = 0;
+    } else {
+        b = search_lanes<L>(a.s.batch, slot, [&](int i) { return (int64_t)(__ldg(a.s.cu + i) >> 4) + 2 * (int64_t)i; });
+        if (b < 0) return;
+        t0 = __ldg(a.s.cu + b);
+        n = (int64_t)__ldg(a.s.cu + b + 1) - t0;
+        j = slot - ((t0 >> 4) + 2 * (int64_t)b);
+        if (t0 < 0 || n < 0 || t0 + n > a.s.tokens) {
+            if (threadIdx.x == 0) report_invalid();
+            return;
+        }
+    }
+    const int64_t len = __ldg(a.s.kv_len + b);
+    int64_t first = len - n;
+    if (first < 0) first = 0;                               // padding rows in front
+    if (first >= len) return;
+    const int64_t blk = (first >> 4) + j;
+    if (blk * kKvBlock >= len) return;
+    if (len > cap) {
+        if (threadIdx.x == 0) report_invalid();
+        if (blk * kKvBlock >= cap) return;
+    }
+    const int64_t page = __ldg(a.s.table + (int64_t)b * a.s.max_pages + (blk * kKvBlock >> a.s.page_shift));
+    if (page < 0 || page >= a.s.pages) {
+        if (threadIdx.x == 0) report_invalid();
+        return;
+    }
+    const int64_t pos = blk * kKvBlock + row;
+    const bool fresh = pos >= first && pos < len;
+    const bool held = blk * kKvBlock < first;               // the block has older tokens
+    const int64_t t = t0 + n - (len - pos);
+    float k[8], v[8], mk = 0.f, mv = 0.f;
+    const int blocks = 1 << (a.s.page_shift - 4), in_page = (int)(blk & (blocks - 1));
+    const int64_t sc = (page * H + h) * blocks + in_page;
+    const float old_k = held ? a.c.ks[sc] : 0.f, old_v = held ? a.c.vs[sc] : 0.f;
+    bool ok = true;
+    if (fresh) {
+        const uint16_t *kp = a.k.p + t * a.k.ts + h * a.k.hs, *vp = a.v.p + t * a.v.ts + h * a.v.hs;
+        const uint2 k0 = __ldg(reinterpret_cast<const uint2 *>(kp + g.a)), k1 = __ldg(reinterpret_cast<const uint2 *>(kp + g.b));
+        const uint2 v0 = __ldg(reinterpret_cast<const uint2 *>(vp + g.a)), v1 = __ldg(reinterpret_cast<const uint2 *>(vp + g.b));
+        float w[8];
+        load_weight(a.kw, g, w);
+        ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.s.tokens, pos, c, s));
+        unpack_bf16x4(k0, k);
+        unpack_bf16x4(k1, k + 4);
+        unpack_bf16x4(v0, v);
+        unpack_bf16x4(v1, v + 4);
+        norm_rotate<L>(k, w, a.kw != nullptr, a.eps, g, a.rope.adjacent, c, s);
+        if (!ok) {
+            if (lane == 0) report_invalid();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mk = fmaxf(mk, fabsf(k[i])), mv = fmaxf(mv, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) {
+        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
+    if (lane == 0) most_k[row] = mk, most_v[row] = mv;
+    __syncthreads();
+    mk = mv = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mk = fmaxf(mk, most_k[i]), mv = fmaxf(mv, most_v[i]);
+    float shrink_k, shrink_v;
+    const float sk = grow_scale(mk, held, old_k, shrink_k), sv = grow_scale(mv, held, old_v, shrink_v);
+    const int64_t at = (sc * kKvBlock + row) * a.c.dim;
+    int8_t *kq = a.c.k + at, *vq = a.c.v + at;
+    if (fresh) {
+        *reinterpret_cast<uint32_t *>(kq + g.a) = codes4(k, sk);
+        *reinterpret_cast<uint32_t *>(kq + g.b) = codes4(k + 4, sk);
+        *reinterpret_cast<uint32_t *>(vq + g.a) = codes4(v, sv);
+        *reinterpret_cast<uint32_t *>(vq + g.b) = codes4(v + 4, sv);
+    } else if (pos < first) {
+        if (shrink_k != 1.f) {
+            uint2 *p = reinterpret_cast<uint2 *>(kq + 8 * lane);
+            const uint2 w = *p;
+            *p = make_uint2(rescale4(w.x, shrink_k), rescale4(w.y, shrink_k));
+        }
+        if (shrink_v != 1.f) {
+            uint2 *p = reinterpret_cast<uint2 *>(vq + 8 * lane);
+            const uint2 w = *p;
+            *p = make_uint2(rescale4(w.x, shrink_v), rescale4(w.y, shrink_v));
+        }
+    }
+    if (threadIdx.x == 0) a.c.ks[sc] = sk, a.c.vs[sc] = sv;
+}
+
+cudaError_t launch_kv8_append(const AppendArgs &a, int sms, cudaStream_t stream) {
+    const int L = a.c.dim / 8;
+    const int64_t slots = a.s.cu ? a.s.tokens / kKvBlock + 2 * (int64_t)a.s.batch : a.s.batch;
+    const int64_t kv_ctas = slots * a.c.heads;
+    const int per = a.q_heads ? heads_per_group(a.s.tokens, a.q_heads, L, sms) : 1;
+    const int chunks = (a.q_heads + per - 1) / per;
+    const int64_t blocks = kv_ctas + (a.s.tokens * chunks + 15) / 16;
+    if (L == 16)
+        kv8_append_kernel<16><<<(unsigned)blocks, 16 * 16, 0, stream>>>(a, kv_ctas, per, chunks);
+    else
+        kv8_append_kernel<8><<<(unsigned)blocks, 16 * 8, 0, stream>>>(a, kv_ctas, per, chunks);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------ read
+// Eight codes to BF16: fl(q * s) rounded once more to BF16.
+__device__ __forceinline__ uint4 dequant8(const uint2 &w, float s) {
+    const uint32_t x[2] = {w.x, w.y};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = x[i >> 1] >> (16 * (i & 1));
+        r[i] = pack_bf16x2((float)(int8_t)b * s, (float)(int8_t)(b >> 8) * s);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <int L>
+__global__ void __launch_bounds__(kHeadThreads) kv8_read_kernel(const __grid_constant__ ReadArgs a, int per, int chunks) {
+    const int lane = threadIdx.x & (L - 1);
+    const int64_t task = (int64_t)blockIdx.x * (kHeadThreads / L) + threadIdx.x / L;
+    const int64_t t = task / chunks;
+    if (t >= a.s.tokens) return;
+    const TokenPlace p = place_token<L>(a.s, t);
+    if (p.b < 0) return;
+    const int H = a.c.heads, D = 8 * L;
+    int64_t page = -1;
+    if (p.pos >= 0) {
+        if (p.pos < (int64_t)a.s.max_pages << a.s.page_shift)
+            page = __ldg(a.s.table + (int64_t)p.b * a.s.max_pages + (p.pos >> a.s.page_shift));
+        if (page < 0 || page >= a.s.pages) {
+            if (lane == 0) report_invalid();
+            page = -1;
+        }
+    }
+    const int in_page = (int)(p.pos & ((1 << a.s.page_shift) - 1));
+    const int h0 = (int)(task - t * chunks) * per, h1 = min(h0 + per, H);
+    for (int h = h0; h < h1; ++h) {
+        uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+        if (page >= 0) {
+            const int64_t r = ((page * H + h) << a.s.page_shift) + in_page;
+            const float ks = __ldg(a.c.ks + (r >> 4)), vs = __ldg(a.c.vs + (r >> 4));
+            const uint2 kc = __ldg(reinterpret_cast<const uint2 *>(a.c.k + r * D) + lane);
+            const uint2 vc = __ldg(reinterpret_cast<const uint2 *>(a.c.v + r * D) + lane);
+            k = dequant8(kc, ks);
+            v = dequant8(vc, vs);
+        }
+        const int64_t o = (t * H + h) * L + lane;
+        if (a.k_out) reinterpret_cast<uint4 *>(a.k_out)[o] = k;
+        if (a.v_out) reinterpret_cast<uint4 *>(a.v_out)[o] = v;
+    }
+}
+
+cudaError_t launch_kv8_read(const ReadArgs &a, int sms, cudaStream_t stream) {
+    const int L = a.c.dim / 8;
+    const int per = heads_per_group(a.s.tokens, a.c.heads, L, sms);
+    const int chunks = (a.c.heads + per - 1) / per;
+    const int64_t blocks = (a.s.tokens * chunks + kHeadThreads / L - 1) / (kHeadThreads / L);
+    if (L == 16)
+        kv8_read_kernel<16><<<(unsigned)blocks, kHeadThreads, 0, stream>>>(a, per, chunks);
+    else
+        kv8_read_kernel<8><<<(unsigned)blocks, kHeadThreads, 0, stream>>>(a, per, chunks);
+    return cudaGetLastError();
+}
+
+}  // namespace convrot

@@ -1,0 +1,607 @@
+"""The attention-side operators on the GPU against their definitions in 64
+bits: head norms with rotation, the paged INT8 cache, attention over it."""
+import numpy as np
+import pytest
+import torch
+
+import rotated_int8_quantized_b200 as cr
+from kv8_reference import BLOCK, Paged, attention, bits_to_f64, norm_rotate
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(autouse=True)
+def status_word_is_clean():
+    cr.load_library().convrot_device_status(None)
+    yield
+
+
+def _randn(*shape, seed=0, outliers=False):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(*shape, generator=g)
+    if outliers:
+        x[..., 3::29] *= 8
+    return x.bfloat16().to(DEV)
+
+
+# A value goes through a norm (a sum of dim squares: relative error below (dim / 8 + 8) 2^-24, the root halves it), three
+# products and a sum of two in FP32: below 24 roundings of 2^-24 of the row's largest pair, then one rounding to BF16.
+def _near_bf16(got, want, scale):
+    err = np.abs(bits_to_f64(got) - want)
+    assert (err <= 2.0 ** -8 * np.abs(want) + 24 * 2.0 ** -24 * scale).all(), err.max()
+
+
+@pytest.mark.parametrize("dim,rot", [(128, 128), (128, 64), (128, 8), (64, 64), (64, 24)])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("tokens,hq,hk,axes,norm", [(1, 1, 0, 1, True), (13, 5, 1, 3, True), (70, 8, 2, 1, False)])
+def test_norm_rope(dim, rot, adjacent, tokens, hq, hk, axes, norm):
+    qkv = _randn(tokens, hq + 2 * hk, dim, seed=tokens, outliers=True)
+    q, k = qkv[:, :hq], qkv[:, hq:hq + hk] if hk else None
+    w = (1 + 0.3 * torch.randn(2, dim, generator=torch.Generator().manual_seed(1))).bfloat16().to(DEV) if norm else [None, None]
+    table = cr.rope_table(50, rot, 1e4)
+    pos = torch.randint(0, 50, (axes, tokens), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    axis = torch.randint(0, axes, (rot // 2,), generator=torch.Generator().manual_seed(3), dtype=torch.uint8) if axes > 1 else None
+    rope = cr.Rope(table, adjacent, None if axis is None else axis.to(DEV))
+    qo, ko = cr.qk_norm_rope(q, k, w[0], w[1], 1e-5, rope, pos.to(DEV))
+    for x, y, wt in ((q, qo, w[0]), (k, ko, w[1])):
+        if x is None:
+            assert y is None
+            continue
+        ref = norm_rotate(bits_to_f64(x), None if wt is None else bits_to_f64(wt), 1e-5, table.cpu().numpy().astype(np.float64),
+                          pos.numpy(), None if axis is None else axis.numpy(), adjacent)
+        _near_bf16(y, ref, np.abs(ref).max(-1, keepdims=True))
+    # in place, and the same bits
+    cr.QKNormRope(q, k, q, k, w[0], w[1], 1e-5, rope, pos.to(DEV))()
+    assert torch.equal(q, qo) and (k is None or torch.equal(k, ko))
+
+
+def test_norm_rope_many_heads_take_eight_rows_a_group():
+    q, k = _randn(2100, 42, 128), _randn(2100, 42, 128, seed=1)
+    table, pos = cr.rope_table(2100, 128, 1e6), torch.arange(2100, dtype=torch.int32, device=DEV)
+    w = _randn(128, seed=2)
+    qo, ko = cr.qk_norm_rope(q, k, w, None, rope=cr.Rope(table), positions=pos)
+    for x, y, wt in ((q, qo, w), (k, ko, None)):
+        ref = norm_rotate(bits_to_f64(x), None if wt is None else bits_to_f64(wt), 1e-6, table.cpu().numpy().astype(np.float64),
+                          pos.cpu().numpy()[None], None, False)
+        _near_bf16(y, ref, np.abs(ref).max(-1, keepdims=True))
+
+
+def test_norm_only_and_broadcast_input():
+    q = _randn(1, 1, 64).expand(9, 3, 64)
+    w = _randn(64, seed=2)
+    qo, _ = cr.qk_norm_rope(q, None, w)
+    ref = norm_rotate(bits_to_f64(q), bits_to_f64(w), 1e-6, None, None, None, False)
+    _near_bf16(qo, ref, np.abs(ref).max(-1, keepdims=True))
+
+
+def test_positions_outside_the_table_give_zero_rows():
+    q = _randn(4, 2, 64)
+    rope = cr.Rope(cr.rope_table(10, 64))
+    pos = torch.tensor([0, 10, 9, -1], dtype=torch.int32, device=DEV)
+    out, _ = cr.qk_norm_rope(q, None, rope=rope, positions=pos)
+    assert out[1].abs().max() == 0 and out[3].abs().max() == 0
+    assert torch.equal(out[0], q[0]) and out[2].abs().max() > 0
+    with pytest.raises(cr.ConvrotError) as e:
+        cr.convrot_device_status()
+    assert e.value.status == 1
+    cr.convrot_device_status()
+
+
+# ------------------------------------------------------------------ append
+def _append(paged, news, hq, hk, dim, seed, rope=None, w=None, cu="cu", v_scale=1.0, k=None, v=None):
+    """Appends `news` tokens to every sequence (lens grow); returns what went in."""
+    total = sum(news)
+    qkv = _randn(total, hq + 2 * hk, dim, seed=seed, outliers=True)
+    q, kk, vv = qkv[:, :hq] if hq else None, qkv[:, hq:hq + hk], qkv[:, hq + hk:] * v_scale
+    kk, vv = (kk if k is None else k), (vv if v is None else v)
+    old = list(paged.lens)
+    paged.lens = [a + b for a, b in zip(old, news)]
+    paged.kv_len = torch.tensor(paged.lens, dtype=torch.int32, device=DEV)
+    cus = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV) if cu == "cu" else None
+    before = [x.clone() for x in (paged.cache.k, paged.cache.v, paged.cache.k_scale, paged.cache.v_scale)]
+    out = cr.kv8_append(q, kk, vv, paged.cache, paged.table_dev, paged.kv_len, cus, w, w, 1e-6, rope)
+    return q, kk, vv, out, old, before
+
+
+def _check_append(paged, news, k_ref, v_ref, old, before):
+    """Codes and scales of the touched blocks, and that nothing else changed."""
+    page = paged.page
+    for which, ref in ((0, k_ref), (1, v_ref)):
+        codes, scales = (paged.cache.k, paged.cache.v)[which].cpu().numpy(), (paged.cache.k_scale, paged.cache.v_scale)[which].cpu().numpy()
+        codes0, scales0 = before[which].cpu().numpy(), before[2 + which].cpu().numpy()
+        same, same_s = codes == codes0, (scales == scales0) | (np.isnan(scales) & np.isnan(scales0))
+        t = 0
+        for b, n in enumerate(news):
+            p = old[b]
+            while p < old[b] + n:
+                off = p % BLOCK
+                m = min(BLOCK - off, old[b] + n - p)
+                pg, row = int(paged.table[b, p // page]), p % page // BLOCK
+                lo = p % page - off
+                x = ref[t:t + m]                                         # [m, heads, dim]
+                s, c = scales[pg, :, row].astype(np.float64), codes[pg, :, lo + off:lo + off + m].astype(np.float64)
+                most = np.abs(x).max((0, 2))
+                if off == 0:
+                    # amax / 127, the values of x within 24 FP32 roundings
+                    assert (np.abs(s - most / 127) <= 32 * 2.0 ** -24 * most / 127).all()
+                else:
+                    s0 = scales0[pg, :, row].astype(np.float64)
+                    j = np.log2(s / s0)
+                    assert (j == np.rint(j)).all() and (j >= 0).all()
+                    assert (most < 127.5 * s * (1 + 2.0 ** -19)).all()
+                    assert ((j == 0) | (most >= 127.5 * s / 2 * (1 - 2.0 ** -19))).all()
+                    c0 = codes0[pg, :, lo:lo + off].astype(np.float64)
+                    assert np.array_equal(codes[pg, :, lo:lo + off], np.rint(c0 / 2.0 ** j[:, None, None]))
+                # half a step, and the FP32 error of x / s (at most 128 * 32 * 2^-24)
+                err = np.abs(c * s[:, None, None] - x.transpose(1, 0, 2))
+                clamped = np.abs(c) == 127
+                assert (err <= s[:, None, None] * np.where(clamped, 0.5 + 2.0 ** -10, 0.5 + 2.0 ** -12)).all()
+                same[pg, :, lo:lo + off + m] = True
+                same_s[pg, :, row] = True
+                p, t = p + m, t + m
+        assert same.all() and same_s.all()
+
+
+@pytest.mark.parametrize("dim,hq,hk,page", [(128, 8, 2, 64), (64, 3, 3, 16), (128, 2, 1, 256)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_append(dim, hq, hk, page, norm):
+    lens, news = [0, 5, 16, 100, 31, 0, 240], [3, 1, 33, 28, 1, 0, 70]
+    paged = _roomy(lens, [a + b for a, b in zip(lens, news)], hk, dim, page)
+    table = cr.rope_table(400, dim, 1e4)
+    w = _randn(dim, seed=9) if norm else None
+    q, k, v, out, old, before = _append(paged, news, hq, hk, dim, 4, cr.Rope(table), w)
+    pos = np.concatenate([np.arange(a, a + n) for a, n in zip(old, news)])
+    wt = None if w is None else bits_to_f64(w)
+    cs = table.cpu().numpy().astype(np.float64)
+    kr = norm_rotate(bits_to_f64(k), wt, 1e-6, cs, pos[None], None, False)
+    qr = norm_rotate(bits_to_f64(q), wt, 1e-6, cs, pos[None], None, False)
+    _near_bf16(out, qr, np.abs(qr).max(-1, keepdims=True))
+    _check_append(paged, news, kr, bits_to_f64(v), old, before)
+    # the same call again stores the same
+    after = [x.clone() for x in (paged.cache.k, paged.cache.v, paged.cache.k_scale, paged.cache.v_scale)]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV)
+    cr.kv8_append(q, k, v, paged.cache, paged.table_dev, paged.kv_len, cu, w, w, 1e-6, cr.Rope(table))
+    for x, y in zip(after[:2], (paged.cache.k, paged.cache.v)):
+        assert torch.equal(x, y)
+    for x, y in zip(after[2:], (paged.cache.k_scale, paged.cache.v_scale)):
+        assert torch.equal(x.nan_to_num(), y.nan_to_num())
+    cr.convrot_device_status()
+
+
+def _roomy(lens, need, hk, dim, page, seed=0):
+    """A cache with pages for `need` tokens of which `lens` are stored."""
+    paged = Paged(need, hk, dim, page, seed)
+    paged.lens = list(lens)
+    paged.kv_len = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    return paged
+
+
+def test_append_token_by_token_stays_within_a_step():
+    """Sixteen calls fill a block, every token larger than the last: each value ends within one step of its block's
+    scale, the bound that doubling gives."""
+    hk, dim = 2, 64
+    paged = _roomy([0], [40], hk, dim, 16)
+    rows_k, rows_v = [], []
+    for i in range(40):
+        k = _randn(1, hk, dim, seed=100 + i) * float(1.13 ** i)
+        v = _randn(1, hk, dim, seed=200 + i) * float(1.5 ** (i % 16) if i < 32 else 0.0)
+        rows_k.append(bits_to_f64(k))
+        rows_v.append(bits_to_f64(v))
+        _append(paged, [1], 0, hk, dim, 0, cu=None, k=k, v=v)
+    for which, rows in ((0, rows_k), (1, rows_v)):
+        got, x = paged.values(0, which), np.concatenate(rows)
+        s = (paged.cache.k_scale, paged.cache.v_scale)[which].cpu().numpy()
+        for t in range(40):
+            step = s[int(paged.table[0, t // 16]), :, 0][:, None]
+            assert (np.abs(got[t] - x[t]) <= step * (1 + 2.0 ** -10)).all()
+    assert (paged.values(0, 1)[32:] == 0).all()          # all-zero block: scale 0
+    cr.convrot_device_status()
+
+
+def test_append_after_a_block_of_zeros_and_far_larger_values():
+    hk, dim = 1, 64
+    paged = _roomy([0], [16], hk, dim, 16)
+    zero = torch.zeros(1, hk, dim, dtype=torch.bfloat16, device=DEV)
+    small, large = _randn(1, hk, dim) * 2.0 ** -60, _randn(1, hk, dim, seed=1) * 2.0 ** 20
+    for x in (zero, small, zero, large, small):
+        _append(paged, [1], 0, hk, dim, 0, cu=None, k=x, v=x)
+    got = paged.values(0, 0)
+    s = float(paged.cache.k_scale[int(paged.table[0, 0]), 0, 0])
+    assert abs(s - float(large.abs().max()) / 127) <= 2.0 ** -22 * s
+    assert (got[[0, 1, 2, 4]] == 0).all() and np.abs(got[3] - bits_to_f64(large)[0]).max() <= s / 2 * (1 + 2.0 ** -10)
+
+
+def test_append_padding_and_what_it_leaves_alone():
+    hk, hq, dim = 2, 4, 64
+    paged = _roomy([0, 7, 0], [16, 32, 16], hk, dim, 16)
+    # single tokens, the first and last slots idle (kv_len 0)
+    q, k, v = (_randn(3, h, dim, seed=h) for h in (hq, hk, hk))
+    kv_len = torch.tensor([0, 8, 0], dtype=torch.int32, device=DEV)
+    before = paged.cache.k.clone()
+    out = cr.kv8_append(q, k, v, paged.cache, paged.table_dev, kv_len, rope=cr.Rope(cr.rope_table(16, 64)))
+    assert out[0].abs().max() == 0 and out[2].abs().max() == 0 and out[1].abs().max() > 0
+    changed = (paged.cache.k != before).any(-1).any(1)
+    page = int(paged.table[1, 0])
+    assert changed.nonzero().tolist() in ([[page, r] for r in range(8)], [[page, 7]])
+    # rows behind the last sequence stay as they were
+    x = torch.full((6, hq, dim), 7.0, dtype=torch.bfloat16, device=DEV)
+    cu = torch.tensor([0, 2, 3, 3], dtype=torch.int32, device=DEV)
+    q, k, v = (_randn(6, h, dim, seed=h) for h in (hq, hk, hk))
+    kv_len = torch.tensor([2, 9, 0], dtype=torch.int32, device=DEV)
+    before = paged.cache.v.clone()
+    cr.KV8Append(q, k, v, paged.cache, paged.table_dev, kv_len, x, cu=cu)()
+    assert (x[3:] == 7).all() and torch.equal(x[:3], q[:3])
+    assert (paged.cache.v != before).any(-1).any(1).sum() <= 2 + 9
+    cr.convrot_device_status()
+
+
+def test_append_bad_pages_are_recorded_and_skipped():
+    hk, dim = 1, 64
+    paged = _roomy([0, 0], [40, 40], hk, dim, 16)
+    table = paged.table_dev.clone()
+    table[0, 1] = 10 ** 6
+    table[1, 0] = -3
+    k, v = _randn(80, hk, dim), _randn(80, hk, dim, seed=1)
+    cu = torch.tensor([0, 40, 80], dtype=torch.int32, device=DEV)
+    kv = torch.tensor([40, 40], dtype=torch.int32, device=DEV)
+    before = paged.cache.k.clone()
+    cr.kv8_append(None, k, v, paged.cache, table, kv, cu)
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+    changed = {r for r in (paged.cache.k != before).flatten(1).any(1).nonzero()[:, 0].tolist()}
+    assert changed == {int(paged.table[0, 0]), int(paged.table[0, 2]), int(paged.table[1, 1]), int(paged.table[1, 2])}
+    # longer than its row of the table
+    kv = torch.tensor([table.shape[1] * 16 + 5, 40], dtype=torch.int32, device=DEV)
+    cr.kv8_append(None, k, v, paged.cache, paged.table_dev, kv, cu)
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+    # cu that is no partition of the rows: recorded, nothing out of bounds
+    cr.kv8_append(None, k, v, paged.cache, paged.table_dev, torch.tensor([40, 40], dtype=torch.int32, device=DEV),
+                  torch.tensor([0, 90, 200], dtype=torch.int32, device=DEV))
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+
+
+# ------------------------------------------------------------------ read
+@pytest.mark.parametrize("dim,hk,page", [(128, 2, 64), (64, 5, 16)])
+def test_read(dim, hk, page):
+    lens = [1, 0, 37, 130, 64]
+    paged = Paged(lens, hk, dim, page)
+    back = [1, 0, 20, 130, 1]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(back)]), dtype=torch.int32, device=DEV)
+    k, v = cr.kv8_read(paged.cache, paged.table_dev, paged.kv_len, sum(back) + 3, cu)
+    for which, got in ((0, k), (1, v)):
+        ref = np.concatenate([paged.values(b, which)[n - m:] for b, (n, m) in enumerate(zip(lens, back))])
+        # the product in FP32 (2^-24) and its rounding to BF16 (2^-8)
+        err = np.abs(bits_to_f64(got)[:sum(back)] - ref)
+        assert (err <= (2.0 ** -8 + 2.0 ** -23) * np.abs(ref)).all()
+        assert (got[sum(back):] == 0).all()                # rows behind: as they were
+    only, _ = cr.kv8_read(paged.cache, paged.table_dev, paged.kv_len)
+    assert (only[1] == 0).all()                            # an empty sequence's row
+    assert torch.equal(only[[0, 2, 3, 4]], k[(cu[1:][[0, 2, 3, 4]] - 1).long()])
+    cr.convrot_device_status()
+    table = paged.table_dev.clone()
+    table[3, 0] = 99
+    out = torch.ones(130, hk, dim, dtype=torch.bfloat16, device=DEV)
+    cr.KV8Read(paged.cache, table[3:4], paged.kv_len[3:4].clone(), out, None,
+               cu=torch.tensor([0, 130], dtype=torch.int32, device=DEV))()
+    assert (out[:page] == 0).all() and (out[page:] != 0).any()
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+
+
+# ------------------------------------------------------------------ attention
+def _check_attention(paged, q, out, lse, news, causal, scale, rows=None):
+    """Every row (or `rows` of them per sequence, the last among them) against the definition.
+
+    The weights are rounded to FP16 (2^-12 of each, and exp2 and the products around it less than that again: 2^-11 of
+    sum p|v| in all); a score is off by FP32 roundings of sums of |q k|, at most 2^-20 of the largest, which moves a
+    weight and the weights' sum by that much each; the result is rounded to BF16 (2^-8).  lse: the score's error and
+    FP32 roundings of a sum of weights and of the logarithm.
+
+    FP16 ends at 2^-24, and a weight (times its value scale) is held as 2^7 of its share of the running maximum, so
+    each is off by up to half of 2^-24 / 2^7 of that maximum, which is at most the sequence's largest value scale; a
+    code is at most 127 and the weights' sum at least 1: 2^-32 * 127 * tokens * largest scale in all."""
+    t = 0
+    o, z = bits_to_f64(out), lse.cpu().numpy().astype(np.float64)
+    qf = bits_to_f64(q)
+    for b, n in enumerate(news):
+        k, v = paged.values(b, 0), paged.values(b, 1)
+        used = paged.table.numpy()[b][:-(-paged.lens[b] // paged.page)]
+        lost = 2.0 ** -32 * 127 * paged.lens[b] * np.nanmax(paged.cache.v_scale.cpu().numpy()[used], initial=0)
+        pick = range(n) if rows is None or n <= rows else sorted(set(np.linspace(0, n - 1, rows).astype(int)))
+        for i in pick:
+            # row i alone: a causal row sees len - n + i + 1 tokens
+            m = max(0, paged.lens[b] - n + i + 1) if causal else paged.lens[b]
+            ref, rl, mag, reach = attention(qf[t + i:t + i + 1], k[:m], v[:m], 1, False, scale)
+            err = np.abs(o[t + i] - ref[0])
+            tol = 2.0 ** -8 * np.abs(ref[0]) + (2.0 ** -11 + 2.0 ** -18 * reach[0][:, None]) * mag[0] + lost
+            assert (err <= tol).all(), (b, i, (err - tol).max())
+            if m == 0:
+                assert (o[t + i] == 0).all() and (z[t + i] == -np.inf).all()
+            else:
+                assert (np.abs(z[t + i] - rl[0]) <= 2.0 ** -18 * (1 + np.abs(rl[0]) + reach[0])).all()
+        t += n
+
+
+def _attend(lens, news, hq, hk, dim, page, causal=True, scale=None, seed=0, cu=True, q=None, **kw):
+    paged = Paged(lens, hk, dim, page, seed)
+    q = _randn(sum(news), hq, dim, seed=seed + 1) * 2 if q is None else q
+    cus = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV) if cu else None
+    out, lse = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cus, scale, causal)
+    cr.convrot_device_status()
+    _check_attention(paged, q, out, lse, news, causal, dim ** -0.5 if scale is None else scale, **kw)
+    return paged, q, out, lse, cus
+
+
+LENS = [1, 0, 15, 16, 17, 63, 64, 65, 129, 700]
+
+
+@pytest.mark.parametrize("dim,hq,hk,page", [(128, 8, 1, 64), (128, 8, 8, 16), (64, 12, 4, 32), (64, 16, 1, 256),
+                                            (128, 10, 2, 128), (128, 40, 2, 64)])
+def test_attention_single_tokens(dim, hq, hk, page):
+    _attend(LENS, [1] * len(LENS), hq, hk, dim, page, cu=False)
+
+
+@pytest.mark.parametrize("length", [1, 16, 50, 577, 4099])
+def test_attention_one_sequence_is_split(length):
+    _attend([length], [1], 16, 2, 128, 16, cu=False)
+
+
+@pytest.mark.parametrize("dim,hq,hk,page", [(128, 8, 1, 64), (64, 6, 2, 16)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_short_runs(dim, hq, hk, page, causal):
+    lens, news = [5, 40, 0, 130, 33, 3], [5, 3, 0, 7, 1, 2]
+    _attend(lens, news, hq, hk, dim, page, causal)
+
+
+@pytest.mark.parametrize("dim,hq,hk,page", [(128, 8, 1, 64), (64, 3, 3, 16), (128, 14, 2, 32)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_prompts(dim, hq, hk, page, causal):
+    lens, news = [130, 1, 300, 17, 64], [130, 1, 45, 17, 63]
+    _attend(lens, news, hq, hk, dim, page, causal, rows=12)
+
+
+@pytest.mark.parametrize("dim,hq,hk", [(128, 8, 1), (64, 2, 2), (128, 3, 1)])
+def test_attention_a_long_prompt(dim, hq, hk):
+    _attend([1111], [1111], hq, hk, dim, 64, rows=9)
+    _attend([1500], [777], hq, hk, dim, 64, rows=9, causal=False)
+
+
+def test_attention_mixes_prompts_and_single_tokens():
+    _attend([900, 1, 400, 77, 0, 2000], [300, 1, 1, 1, 0, 1], 16, 2, 128, 64, rows=7)
+
+
+def test_attention_rows_before_the_sequence_see_nothing():
+    # more rows than tokens: the first see nothing under a causal mask
+    _attend([3, 0, 20], [9, 4, 40], 8, 2, 64, 16)
+    _attend([3, 0, 20], [9, 4, 40], 8, 2, 64, 16, causal=False)
+    _attend([100, 130], [300, 130], 8, 1, 128, 16, rows=11)
+
+
+def test_attention_score_ranges():
+    """Sharp softmax, scores far from zero, queries over many binades."""
+    for factor in (40.0, 2.0 ** -30, 2.0 ** 12):
+        q = _randn(3, 8, 128) * factor
+        _attend([70, 300, 1], [1, 1, 1], 8, 1, 128, 16, cu=False, q=q)
+    q = _randn(200, 8, 128)
+    q[..., ::2] *= 2.0 ** -12
+    q[..., 5] *= 64
+    _attend([300], [200], 8, 1, 128, 64, q=q, rows=9)
+    q[3] = 0
+    _attend([300], [200], 8, 1, 128, 64, q=q, scale=3.0, rows=9)
+
+
+def test_attention_value_scales_over_many_binades():
+    lens = [200, 300]
+    for news in ([1, 1], [190, 250]):
+        paged = Paged(lens, 1, 128, 16)
+        g = torch.Generator().manual_seed(5)
+        shape = paged.cache.v_scale.shape
+        s = torch.ldexp(paged.cache.v_scale.cpu().nan_to_num(1.0), torch.randint(-30, 10, shape, generator=g))
+        s[torch.rand(shape, generator=g) < 0.2] = 0
+        paged.cache.v_scale.copy_(s)
+        paged.cache.v[(s == 0).to(DEV).repeat_interleave(BLOCK, -1)] = 0
+        q = _randn(sum(news), 8, 128) * 2
+        cu = torch.tensor([0, news[0], sum(news)], dtype=torch.int32, device=DEV)
+        out, lse = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu)
+        _check_attention(paged, q, out, lse, news, True, 128 ** -0.5, rows=9)
+
+
+def test_attention_a_nan_query_stays_in_its_row():
+    for lens, news in (([50, 90], [1, 1]), ([200, 90], [150, 64])):
+        paged, q, out, lse, cu = _attend(lens, news, 8, 2, 128, 16, rows=3)
+        bad = q.clone()
+        bad[news[0], 3, 7] = float("nan")
+        bad[0, 1, 0] = float("inf")
+        out2, lse2 = cr.attn_kv8(bad, paged.cache, paged.table_dev, paged.kv_len, cu)
+        hit = torch.zeros(out.shape[:2], dtype=torch.bool, device=DEV)
+        hit[news[0], 3] = hit[0, 1] = True
+        assert out2[hit].isnan().all()
+        assert torch.equal(out2[~hit], out[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
+def test_attention_strided_queries_and_rows_behind():
+    hq, hk, dim = 8, 2, 128
+    paged = Paged([150, 33], hk, dim, 32)
+    for news, total in (([1, 1], None), ([140, 33], 180), ([5, 2], 9)):
+        rows = total or 2
+        qkv = _randn(rows, hq + 2 * hk, dim)
+        q = qkv[:, :hq]
+        cu = None if total is None else torch.tensor([0, news[0], sum(news)], dtype=torch.int32, device=DEV)
+        out = torch.full((rows, hq, dim), 3.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((rows, hq), 3.0, device=DEV)
+        cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, cu=cu, lse=lse)()
+        ref, _ = cr.attn_kv8(q.contiguous(), paged.cache, paged.table_dev, paged.kv_len, cu)
+        n = sum(news)
+        assert torch.equal(out[:n], ref[:n]) and (out[n:] == 3).all() and (lse[n:] == 3).all()
+        _check_attention(paged, q, out, lse, news, True, dim ** -0.5, rows=9)
+        # head-major queries
+        qt = q.transpose(0, 1).contiguous().transpose(0, 1)
+        out2, _ = cr.attn_kv8(qt, paged.cache, paged.table_dev, paged.kv_len, cu)
+        assert torch.equal(out2[:n], ref[:n])
+
+
+def test_attention_bad_device_arguments_are_recorded():
+    hq, hk, dim = 4, 2, 64
+    for lens, news in (([100, 60], [1, 1]), ([100, 60], [90, 60])):
+        paged = Paged(lens, hk, dim, 16)
+        q = _randn(sum(news), hq, dim)
+        cu = torch.tensor([0, news[0], sum(news)], dtype=torch.int32, device=DEV)
+        good, _ = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu)
+        cr.convrot_device_status()
+        table = paged.table_dev.clone()
+        table[0, 2] = paged.cache.k.shape[0]
+        table[0, 3] = -7
+        out, _ = cr.attn_kv8(q, paged.cache, table, paged.kv_len, cu)
+        assert torch.equal(out[news[0]:], good[news[0]:]) and out.isfinite().all()
+        with pytest.raises(cr.ConvrotError):
+            cr.convrot_device_status()
+        for kv in ([10 ** 6, 60], [-5, 60]):
+            out, _ = cr.attn_kv8(q, paged.cache, paged.table_dev, torch.tensor(kv, dtype=torch.int32, device=DEV), cu)
+            assert torch.equal(out[news[0]:], good[news[0]:])
+            with pytest.raises(cr.ConvrotError):
+                cr.convrot_device_status()
+        for bad in ([0, 10 ** 6, 10 ** 6], [0, sum(news), sum(news) - 1], [-4, 1, sum(news)]):
+            cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, torch.tensor(bad, dtype=torch.int32, device=DEV))
+            with pytest.raises(cr.ConvrotError):
+                cr.convrot_device_status()
+
+
+def test_attention_bits_do_not_change_between_runs_and_the_workspace_is_reused():
+    lens, news = [3000, 10, 700], [1, 1, 1]
+    paged = Paged(lens, 2, 128, 64)
+    q = _randn(3, 16, 128)
+    out, lse = torch.empty_like(q), torch.empty(3, 16, device=DEV)
+    call = cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, lse=lse)
+    call()
+    first = out.clone(), lse.clone()
+    for _ in range(20):
+        out.zero_()
+        call()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    # other lengths on the same workspace
+    paged.kv_len.copy_(torch.tensor([17, 9, 650]))
+    paged.lens = [17, 9, 650]
+    call()
+    _check_attention(paged, q, out, lse, news, True, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [200, 1, 30]])
+def test_a_captured_step_follows_its_tensors(news):
+    """Append and attention in one CUDA graph: replays take new lengths and values from the same tensors."""
+    hq, hk, dim, page = 8, 2, 128, 16
+    lens = [230, 40, 100]
+    paged = _roomy(lens, [600, 600, 600], hk, dim, page)
+    total = sum(news)
+    qkv = _randn(total, hq + 2 * hk, dim)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    rot, out, lse = torch.empty(total, hq, dim, dtype=torch.bfloat16, device=DEV), None, torch.empty(total, hq, device=DEV)
+    out = torch.empty_like(rot)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV)
+    rope = cr.Rope(cr.rope_table(600, dim))
+    append = cr.KV8Append(q, k, v, paged.cache, paged.table_dev, paged.kv_len, rot, cu=cu, rope=rope)
+    attn = cr.AttnKV8(rot, paged.cache, paged.table_dev, paged.kv_len, out, cu=cu, lse=lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        append()
+        attn()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        append()
+        attn()
+    for step in range(1, 4):
+        lens = [n + 7 * step for n in lens]
+        paged.kv_len.copy_(torch.tensor(lens))
+        # lengths jump by more than the rows: the tokens between hold random codes, give their blocks scales
+        for s in (paged.cache.k_scale, paged.cache.v_scale):
+            s.nan_to_num_(nan=0.01)
+        paged.lens = lens
+        qkv.copy_(_randn(total, hq + 2 * hk, dim, seed=step))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_attention(paged, rot, out, lse, news, True, dim ** -0.5, rows=4)
+    cr.convrot_device_status()
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own, running at the same time."""
+    jobs = []
+    for i, (lens, news) in enumerate((([5000, 3], [1, 1]), ([600, 350], [600, 50]), ([4000], [1]), ([900], [900]))):
+        paged = Paged(lens, 2, 128, 64, seed=i)
+        q = _randn(sum(news), 8, 128, seed=i)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV)
+        call = cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, cu=cu, lse=lse)
+        call()
+        torch.cuda.synchronize()
+        jobs.append((call, out, lse, out.clone(), lse.clone(), torch.cuda.Stream()))
+    for _ in range(10):
+        for call, out, _, _, _, stream in jobs:
+            call(stream)
+    torch.cuda.synchronize()
+    for _, out, lse, ref, ref_lse, _ in jobs:
+        assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+def test_offsets_beyond_32_bits():
+    """Codes of the last pages lie more than 2^32 bytes into the cache."""
+    hk, dim, page = 8, 128, 128
+    pages = 2 ** 32 // (hk * page * dim) + 40
+    cache = cr.make_kv8_cache(pages, hk, dim, page)
+    table = torch.tensor([[pages - 1, 0, pages - 3], [pages - 5, pages - 2, 1]], dtype=torch.int32, device=DEV)
+    news = [300, 200]
+    k, v = _randn(500, hk, dim), _randn(500, hk, dim, seed=1)
+    cu = torch.tensor([0, 300, 500], dtype=torch.int32, device=DEV)
+    kv = torch.tensor(news, dtype=torch.int32, device=DEV)
+    cr.kv8_append(None, k, v, cache, table, kv, cu)
+    kb, vb = cr.kv8_read(cache, table, kv, 500, cu)
+    # within half a step of a block's scale, which is at most its largest value / 127, and the BF16 rounding
+    for x, y in ((k, kb), (v, vb)):
+        assert ((x.float() - y.float()).abs() <= x.float().abs().max() * (0.51 / 127 + 2.0 ** -8)).all()
+    small = Paged(news, hk, dim, page)
+    small.table = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32)
+    at = table.long()
+    small.cache = cr.KV8Cache(*(x[at.flatten()].contiguous() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+    for rows in ([1, 1], [300, 200]):
+        q = _randn(sum(rows), 16, dim)
+        cu = torch.tensor([0, rows[0], sum(rows)], dtype=torch.int32, device=DEV)
+        out, lse = cr.attn_kv8(q, cache, table, kv, cu)
+        small.lens = news
+        _check_attention(small, q, out, lse, rows, True, dim ** -0.5, rows=3)
+
+
+def test_a_layer_from_projections_to_output():
+    """INT8 q/k/v projections, append, attention, INT8 output projection: prompt in two chunks, then single tokens, against
+    the same operators in 64 bits on the values the projections gave."""
+    hq, hk, dim, hidden = 8, 2, 64, 256
+    ws = [(_randn(n * dim, hidden, seed=n).float() * 0.05).bfloat16() for n in (hq, hk, hk)] + \
+         [(_randn(hidden, hq * dim, seed=77).float() * 0.05).bfloat16()]
+    wq = [cr.quantize_weight(w) for w in ws]
+    nq, nk = _randn(dim, seed=5), _randn(dim, seed=6)
+    table, eps = cr.rope_table(200, dim), 1e-6
+    cs = table.cpu().numpy().astype(np.float64)
+    steps = [[50, 20], [33, 7], [1, 1], [1, 1], [1, 1]]
+    paged = _roomy([0, 0], [100, 40], hk, dim, 16)
+    for i, news in enumerate(steps):
+        total = sum(news)
+        x = _randn(total, hidden, seed=i)
+        qkv = [torch.empty(total, w.n, dtype=torch.bfloat16, device=DEV) for w in wq[:3]]
+        cr.LinearBatch([x] * 3, wq[:3], qkv)()
+        q, k, v = (y.view(total, -1, dim) for y in qkv)
+        old = list(paged.lens)
+        paged.lens = [a + b for a, b in zip(old, news)]
+        paged.kv_len = torch.tensor(paged.lens, dtype=torch.int32, device=DEV)
+        cu = torch.tensor([0, news[0], total], dtype=torch.int32, device=DEV)
+        rot = cr.kv8_append(q, k, v, paged.cache, paged.table_dev, paged.kv_len, cu, nq, nk, eps, cr.Rope(table))
+        pos = np.concatenate([np.arange(a, a + n) for a, n in zip(old, news)])[None]
+        ref = norm_rotate(bits_to_f64(q), bits_to_f64(nq), eps, cs, pos, None, False)
+        _near_bf16(rot, ref, np.abs(ref).max(-1, keepdims=True))
+        out, lse = cr.attn_kv8(rot, paged.cache, paged.table_dev, paged.kv_len, cu)
+        _check_attention(paged, rot, out, lse, news, True, dim ** -0.5, rows=5)
+        y = cr.linear_int8(out.view(total, -1), wq[3], cr.make_workspace(total, wq[3]))
+        assert y.isfinite().all()
+    cr.convrot_device_status()
