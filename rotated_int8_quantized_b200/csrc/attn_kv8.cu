@@ -28,6 +28,9 @@ constexpr int kStreamWarps = 4;
 constexpr int kStreamUnit = 16 * kStreamWarps;      // tokens a CTA takes at a time: a block for each warp
 constexpr float kPBias = 7.f;                       // p' is held times 2^7
 constexpr float kLazy = 8.f;                        // the running maximum moves once it is exceeded by 2^8
+// Sequences with at most so many rows (tokens times queries a key head) are
+// streamed, longer ones go through the tensor-core tiles.
+constexpr int kFewRows = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Value scales below this count as this (a block of zeros has scale 0); the
@@ -140,7 +143,7 @@ struct StreamSmem {
 constexpr int stream_ctas(int nt) { return nt == 1 ? 3 : 2; }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a, int few_rows) {
     constexpr int R = 8 * NT, T = kStreamWarps * 32;
     constexpr int CH = D / 64;                       // 16-byte chunks of a K row a lane holds
     constexpr int VW = D / 32;                       // words of a V row a lane holds
@@ -154,6 +157,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
     // units of every sequence, summed; thread i holds sequences [i per, i per + per)
     const int per = (S.batch + T - 1) / T;
     auto seq_units = [&](const SeqInfo &q) {
+        if ((int64_t)q.n * group > few_rows) return 0ll;         // attn_prompt_kernel's
         const int tiles = (int)(((long long)q.n * group + R - 1) / R);
         const int units = q.len > 0 ? (q.len + kStreamUnit - 1) / kStreamUnit : 1;   // empty rows are written too
         return (long long)tiles * units * H;
@@ -526,6 +530,421 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
     }
 }
 
+// ------------------------------------------------------------ many rows a sequence
+//
+// Prompts and chunks of them: two tiles of 128 rows (of one sequence and key
+// head, rows as above) share a pass over the cache in tiles of 128 tokens, on
+// the tcgen05 tensor cores.  Thirteen warps:
+//   0-3, 4-7  softmax of the first and second tile, a thread for each row;
+//   8-11      the cache's codes from global memory to FP16 operands in shared
+//             memory (exact), the next tile's loads in flight meanwhile;
+//   12        one thread that issues the products.
+// S = Q K^T (FP32, tensor memory) is read by the row's thread twice, once for
+// the maximum and once for the weights, which go back as FP16 over S and are
+// the first operand of P V from there.  The second product sums in tensor
+// memory; as its scale (the running maximum) rarely moves by 2^8, the row's
+// thread rescales it in place when it does.  While one tile is in its softmax
+// the tensor cores work on the other.
+// K and V tiles are the same rows of 128 bytes (64 dims) in the 128-byte
+// swizzle; K is read along the dims (K-major), V along the tokens (MN-major).
+// The blocks' scales go through a ring of four, so that a step's are still
+// there, and its barrier's phase still open to be seen, whatever the order in
+// which the warps get on: step j + 4's are written after S of step j + 2,
+// which is after every row's weights of step j + 1.
+constexpr int kPromptWarps = 13;
+constexpr int kPromptRows = 256;                     // two tiles
+constexpr int kKvTile = 128;
+constexpr int kInfoRing = 4;
+
+template <int D>
+struct PromptSmem {
+    uint8_t q[2][D / 64][128 * 128];
+    uint8_t k[2][D / 64][128 * 128];
+    uint8_t v[2][D / 64][128 * 128];
+    // of a tile's blocks: key scale, log2 of the value scale, its inverse
+    float4 info[kInfoRing][kKvTile / 16];
+    unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+    unsigned long long info_full[kInfoRing], drain;
+    uint32_t tmem;
+    int abort, seq, slot;
+};
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 32 columns of tensor memory, in registers when this returns (the empty
+// statements keep their uses behind the wait).
+__device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
+    tmem_ld_32x32b_x32(taddr, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const __grid_constant__ AttnArgs a, int few_rows) {
+    constexpr int DB = D / 64;                       // 128-byte row blocks of an operand
+    constexpr uint32_t kBlockBytes = 128 * 128;
+    extern __shared__ uint8_t smem_raw[];
+    PromptSmem<D> &sm = *reinterpret_cast<PromptSmem<D> *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = a.c.heads, group = a.q_heads / H;
+    const KvSeqs &S = a.s;
+
+    // The tile pair of this CTA; sequence b owns the slots from floor(cu[b] group / 256) + b on.  Last ones first: under a
+    // causal mask they are the longest.
+    const int64_t slots = gridDim.x / H;
+    const int64_t slot = slots - 1 - blockIdx.x / H;
+    const int h = blockIdx.x % H;
+    auto first_slot = [&](int i) {
+        const int64_t t0 = S.cu ? (int64_t)__ldg(S.cu + i) : i;
+        return t0 * group / kPromptRows + i;
+    };
+    if (warp == 0) {
+        const int b = search_lanes<32>(S.batch, slot, first_slot);
+        if (lane == 0) sm.seq = b, sm.slot = b < 0 ? 0 : (int)(slot - first_slot(b));
+    }
+    __syncthreads();
+    const int b = sm.seq;
+    if (b < 0) return;
+    const SeqInfo q = seq_info(S, b);
+    const int64_t rows = (int64_t)q.n * group, row0 = (int64_t)sm.slot * kPromptRows;
+    if (rows <= few_rows || row0 >= rows) return;
+    const int tiles = rows - row0 > 128 ? 2 : 1;
+    // what the last row sees is what any row sees
+    const int64_t last_tok = (min(rows, row0 + kPromptRows) - 1) / group;
+    const int64_t most = a.causal ? max((int64_t)0, min((int64_t)q.len, (int64_t)q.len - q.n + last_tok + 1)) : q.len;
+    const int steps = (int)((most + kKvTile - 1) / kKvTile);
+
+    const uint32_t q_full = smem_addr(&sm.q_full), k_full = smem_addr(sm.k_full), k_empty = smem_addr(sm.k_empty),
+                   v_full = smem_addr(sm.v_full), v_empty = smem_addr(sm.v_empty), s_full = smem_addr(sm.s_full),
+                   p_full = smem_addr(sm.p_full), o_full = smem_addr(sm.o_full), info_full = smem_addr(sm.info_full), drain = smem_addr(&sm.drain);
+    volatile int *abort_flag = &sm.abort;
+    if (tid == 0) {
+        mbar_init(q_full, 128 * tiles);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full + 8 * i, 4);
+            mbar_init(v_full + 8 * i, 4);
+            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 128);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        for (int i = 0; i < kInfoRing; ++i) mbar_init(info_full + 8 * i, 4);
+        mbar_init(drain, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        tmem_alloc(smem_addr(&sm.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)&sm.tmem;
+    const uint32_t tm_s = tmem, tm_o = tmem + 256;
+
+    if (warp < 8) {
+        // ------------------------------------------------ a row each: queries, softmax, output
+        const int t = warp >> 2, r = tid & 127;
+        if (t < tiles) {
+            const int64_t row = row0 + 128 * t + r;
+            const bool in = row < rows;
+            const int64_t tok = in ? row / group : 0;
+            const int head = h * group + (in ? (int)(row - tok * group) : 0);
+            const uint16_t *src = a.q.p + (q.t0 + tok) * a.q.ts + (int64_t)head * a.q.hs;
+            uint4 x[D / 8];
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                x[i] = in ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+            }
+            int e = (int)(__float_as_uint(top) >> 23) - 127;
+            e = e > 127 ? 0 : (e < -100 ? -100 : e);
+            const float up = __int_as_float((127 + 14 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    y[k] = pack_half2(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+                *reinterpret_cast<uint4 *>(&sm.q[t][i / 8][r * 128 + (((i & 7) ^ (r & 7)) << 4)]) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            fence_proxy_async_shared();
+            mbar_arrive(q_full);
+            const float f = a.scale * kLog2e * __int_as_float((127 - 14 + e) << 23);
+            const int64_t seen = !in ? 0 : (a.causal ? (int64_t)q.len - q.n + tok + 1 : q.len);
+            const int vis = (int)max((int64_t)0, min(seen, (int64_t)q.len));
+
+            const uint32_t lanes = (uint32_t)(warp & 3) << 21;                // 32 lanes a warp, in bits 16 and up
+            const uint32_t ts = tm_s + lanes + 128 * t, to = tm_o + lanes + D * t;
+            float m = -INFINITY;
+            uint64_t l2 = 0;
+            bool ok = true;
+            for (int j = 0; j < steps; ++j) {
+                ok = mbar_wait_bounded(info_full + 8 * (j & (kInfoRing - 1)), (j / kInfoRing) & 1, abort_flag) &&
+                     mbar_wait_bounded(s_full + 8 * t, j & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float4 *info = sm.info[j & (kInfoRing - 1)];
+                const int limit = vis - j * kKvTile;
+                const bool masked = __any_sync(0xffffffffu, limit < kKvTile);
+                float top_t = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t s[32];
+                    tmem_read32(ts + 32 * c, s);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float y = -INFINITY;
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                y = fmaxf(y, 32 * c + 16 * k + i < limit ? __uint_as_float(s[16 * k + i]) : -INFINITY);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2)
+                                y = fmaxf(y, fmaxf(__uint_as_float(s[16 * k + i]), __uint_as_float(s[16 * k + i + 1])));
+                        }
+                        const float4 b4 = info[2 * c + k];
+                        // nothing seen in the block: -inf times a zero key scale would be NaN
+                        top_t = fmaxf(top_t, y == -INFINITY ? y : fmaf(y, f * b4.x, b4.y));
+                    }
+                }
+                const bool over = top_t > m + kLazy;
+                if (__any_sync(0xffffffffu, over)) {
+                    const float mn = over ? top_t : m;
+                    const float al = m == mn ? 1.f : ex2(m - mn);
+                    m = mn;
+                    l2 = mul_f32x2(l2, pack_f32x2(al, al));
+                    if (j > 0) {
+                        // this step's S being complete, so is the product before it
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_read32(to + 32 * c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                            tmem_st_32x32b_x32(to + 32 * c, o);
+                        }
+                    }
+                }
+                const float base = kPBias - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t s[32], p[16];
+                    tmem_read32(ts + 32 * c, s);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 b4 = info[2 * c + k];
+                        const float fb = f * b4.x, add = b4.y + base;
+                        const uint64_t f2 = pack_f32x2(fb, fb), a2 = pack_f32x2(add, add);
+                        uint64_t sum = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint64_t d = pack_f32x2(__uint_as_float(s[16 * k + 2 * i]), __uint_as_float(s[16 * k + 2 * i + 1]));
+                            float u, v;
+                            unpack_f32x2(fma_f32x2(d, f2, a2), u, v);
+                            if (masked) {
+                                const int col = 32 * c + 16 * k + 2 * i;
+                                u = col < limit ? u : -INFINITY;
+                                v = col + 1 < limit ? v : -INFINITY;
+                            }
+                            u = ex2(u);
+                            v = ex2(v);
+                            sum = add_f32x2(sum, pack_f32x2(u, v));
+                            p[8 * k + i] = pack_half2(u, v);
+                        }
+                        l2 = fma_f32x2(sum, pack_f32x2(b4.z, b4.z), l2);
+                    }
+                    tmem_st_32x32b_x16(ts + 16 * c, p);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(p_full + 8 * t);
+            }
+            float l0, l1;
+            unpack_f32x2(l2, l0, l1);
+            const float l = l0 + l1;
+            const float inv = l == 0.f ? 0.f : 1.f / l;              // nothing seen: zeros
+            if (steps > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_full + 8 * t, 0, abort_flag));
+            tc_fence_after();
+            const int64_t at = (q.t0 + tok) * a.q_heads + head;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (steps > 0 && ok) {
+                    tmem_read32(to + 32 * c, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                }
+                if (!in) continue;
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + 32 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                    dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (in && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2;
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------ codes to operands
+        // Warp w converts tokens 32 w .. + 31 of a tile: eight rows by 64 codes a step, a lane 16 codes of a row, which
+        // become two of the row's 16-byte chunks; the eight lanes that store together (two rows, even and odd) fill all
+        // eight chunk positions.
+        const int w = warp - 8, rr = lane >> 2, c4 = lane & 3;
+        const int32_t *pages = S.table + (int64_t)b * S.max_pages;
+        const int bshift = S.page_shift - 4, bmask = (1 << bshift) - 1;
+        const int blocks = (q.len + 15) >> 4;
+        uint4 kx[4][DB], vx[4][DB];
+        int64_t sc[2];                               // the warp's two blocks of the tile in flight; -1: none
+        float ks[2], vs[2];
+        auto find = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int blk = j * 8 + 2 * w + i;
+                sc[i] = -1;
+                if (j < steps && blk < blocks) {
+                    const int page = __ldg(pages + (blk >> bshift));
+                    if (page >= 0 && page < S.pages)
+                        sc[i] = (((int64_t)page * H + h) << bshift) + (blk & bmask);
+                    else if (lane == 0)
+                        report_invalid();
+                }
+            }
+        };
+        auto load = [&](const int8_t *base, const float *scales, uint4 (&x)[4][DB], float (&s)[2]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    x[i][d] = sc[i >> 1] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                             : ld_stream16(base + sc[i >> 1] * (16 * D) + (8 * (i & 1) + rr) * D + 64 * d + 16 * c4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[i] = sc[i] < 0 ? 0.f : __ldg(scales + sc[i]);
+        };
+        auto store = [&](uint8_t (*dst)[128 * 128], const uint4 (&x)[4][DB]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const int row = 32 * w + 8 * i + rr;
+                    uint32_t y[8];
+                    codes_to_half(x[i][d].x, y[0], y[1]);
+                    codes_to_half(x[i][d].y, y[2], y[3]);
+                    codes_to_half(x[i][d].z, y[4], y[5]);
+                    codes_to_half(x[i][d].w, y[6], y[7]);
+                    uint8_t *p = dst[d] + row * 128;
+                    *reinterpret_cast<uint4 *>(p + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(p + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+        };
+        find(0);
+        load(a.c.k, a.c.ks, kx, ks);
+        load(a.c.v, a.c.vs, vx, vs);
+        for (int j = 0; j < steps; ++j) {
+            const int st = j & 1;
+            const uint32_t free_parity = ((j >> 1) & 1) ^ 1;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(k_empty + 8 * st, free_parity, abort_flag))) break;
+            store(sm.k[st], kx);
+            if (lane < 2) {
+                const bool none = (lane ? sc[1] : sc[0]) < 0;
+                const float ve = fmaxf(lane ? vs[1] : vs[0], kLeastScale);
+                sm.info[j & (kInfoRing - 1)][2 * w + lane] =
+                    none ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                         : make_float4(lane ? ks[1] : ks[0], log2f(ve), 1.f / ve, 0.f);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(k_full + 8 * st);
+                mbar_arrive(info_full + 8 * (j & (kInfoRing - 1)));
+            }
+            find(j + 1);
+            load(a.c.k, a.c.ks, kx, ks);
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(v_empty + 8 * st, free_parity, abort_flag))) break;
+            store(sm.v[st], vx);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_full + 8 * st);
+            load(a.c.v, a.c.vs, vx, vs);
+        }
+    } else if (lane == 0 && steps > 0) {
+        // ------------------------------------------------ products
+        constexpr uint32_t idesc_s = idesc_f16(128, kKvTile, false), idesc_o = idesc_f16(128, D, true);
+        const uint32_t q_at = smem_addr(sm.q), k_at = smem_addr(sm.k), v_at = smem_addr(sm.v);
+        auto scores = [&](int t, int st) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t off = (i / 4) * kBlockBytes + (i % 4) * 32;
+                umma_f16(tm_s + 128 * t, smem_desc_k_sw128(q_at + t * DB * kBlockBytes + off),
+                         smem_desc_k_sw128(k_at + st * DB * kBlockBytes + off), idesc_s, i > 0);
+            }
+            umma_commit(s_full + 8 * t);
+        };
+        bool ok = mbar_wait_bounded(q_full, 0, abort_flag) && mbar_wait_bounded(k_full, 0, abort_flag);
+        tc_fence_after();
+        if (ok) {
+            for (int t = 0; t < tiles; ++t) scores(t, 0);
+            if (steps > 2) umma_commit(k_empty);         // waited for by the stage's next use, where there is one
+        }
+        for (int j = 0; ok && j < steps; ++j) {
+            const int st = j & 1, sn = st ^ 1;
+            ok = mbar_wait_bounded(v_full + 8 * st, (j >> 1) & 1, abort_flag);
+            if (ok && j + 1 < steps) ok = mbar_wait_bounded(k_full + 8 * sn, ((j + 1) >> 1) & 1, abort_flag);
+            for (int t = 0; ok && t < tiles; ++t) {
+                ok = mbar_wait_bounded(p_full + 8 * t, j & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kKvTile / 16; ++i)
+                    umma_f16_ts(tm_o + D * t, tm_s + 128 * t + 8 * i,
+                                smem_desc_mn_sw128(v_at + st * DB * kBlockBytes + i * 2048, kBlockBytes), idesc_o, j > 0 || i > 0);
+                if (j + 1 < steps)
+                    scores(t, sn);
+                else
+                    umma_commit(o_full + 8 * t);
+            }
+            if (ok) {
+                if (j + 2 < steps) umma_commit(v_empty + 8 * st);
+                if (j + 3 < steps) umma_commit(k_empty + 8 * sn);
+            }
+        }
+    }
+    // Every product is complete before tensor memory goes: the rows' threads waited for the last ones; a run that gave
+    // up waits here for what it had issued.
+    if (warp == 12 && lane == 0 && *abort_flag) {
+        umma_commit(drain);
+        const unsigned long long start = global_timer_ns();
+        while (!mbar_try_wait(drain, 0) && global_timer_ns() - start < 1000000000ull) {}
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // Rows of a tile: 8 where a sequence has no more, 16 otherwise (the next tile of
 // the same head reads the cache again, mostly from L2).
 static int stream_tiles(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads) {
@@ -544,11 +963,27 @@ static cudaError_t launch_stream(const AttnArgs &a, int sms, cudaStream_t stream
     const int bytes = (int)sizeof(StreamSmem<D, NT>);
     cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    attn_stream_kernel<D, NT><<<sms * stream_ctas(NT), kStreamWarps * 32, bytes, stream>>>(a);
+    attn_stream_kernel<D, NT><<<sms * stream_ctas(NT), kStreamWarps * 32, bytes, stream>>>(a, kFewRows);
+    return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_prompt(const AttnArgs &a, cudaStream_t stream) {
+    const int bytes = (int)sizeof(PromptSmem<D>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t slots = a.s.tokens * (a.q_heads / a.c.heads) / kPromptRows + a.s.batch;
+    attn_prompt_kernel<D><<<(unsigned)(slots * a.c.heads), kPromptWarps * 32, bytes, stream>>>(a, kFewRows);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_kv8(const AttnArgs &a, int sms, cudaStream_t stream) {
+    // a sequence with more rows can only be there if the step has them
+    const int64_t most = a.s.cu ? a.s.tokens : 1;
+    if (most * (a.q_heads / a.c.heads) > kFewRows) {
+        const cudaError_t e = a.c.dim == 128 ? launch_prompt<128>(a, stream) : launch_prompt<64>(a, stream);
+        if (e != cudaSuccess) return e;
+    }
     const int nt = stream_tiles(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
     if (a.c.dim == 128) return nt == 1 ? launch_stream<128, 1>(a, sms, stream) : launch_stream<128, 2>(a, sms, stream);
     return nt == 1 ? launch_stream<64, 1>(a, sms, stream) : launch_stream<64, 2>(a, sms, stream);
