@@ -652,17 +652,24 @@ class _Prepared:
     in them are what the next call works on."""
     _entry = ""
 
-    def _args(self):
-        return (ctypes.byref(self.job),)
+    def _prepare(self, job, device: torch.device, *more) -> None:
+        self.device = device
+        self._call = getattr(load_library(), self._entry)
+        self._args = (ctypes.byref(job),) + more
 
     def __call__(self, stream=None) -> None:
-        fn = getattr(load_library(), self._entry)
-        if torch.cuda.current_device() == self.device.index:
-            status = fn(*self._args(), _stream(stream))
-        else:
+        index = self.device.index
+        if torch.cuda.current_device() != index:
             with torch.cuda.device(self.device):
-                status = fn(*self._args(), _stream(stream))
-        _check(status, self._entry)
+                return self(stream)
+        if stream is None:
+            # the current stream's handle without the Stream object around it (a microsecond of a small call's eight)
+            handle = torch._C._cuda_getCurrentRawStream(index)
+        else:
+            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        status = self._call(*self._args, handle)
+        if status:
+            _check(status, self._entry)
 
 
 class QKNormRope(_Prepared):
@@ -678,8 +685,8 @@ class QKNormRope(_Prepared):
         for name, t, h in (("q", q, heads), ("k", k, j.kv_heads), ("q_out", q_out, heads), ("k_out", k_out, j.kv_heads)):
             _set_rows(j, name, t, h, dim, tokens)
         self.keep = [q, k, q_out, k_out, _set_norm(j, dim, tokens, q_weight, k_weight, eps, rope, positions)]
-        self.device = _one_device(q, k, q_out, k_out, q_weight, k_weight, positions,
-                                  *([rope.cos_sin, rope.axis] if rope else []))
+        self._prepare(j, _one_device(q, k, q_out, k_out, q_weight, k_weight, positions,
+                                     *([rope.cos_sin, rope.axis] if rope else [])))
 
 
 class KV8Append(_Prepared):
@@ -700,8 +707,8 @@ class KV8Append(_Prepared):
             _set_rows(j, name, t, n, h.head_dim, tokens)
         self.keep = [q, k, v, q_out, cache, page_table, kv_len, cu,
                      _set_norm(j, h.head_dim, tokens, q_weight, k_weight, eps, rope, positions)]
-        self.device = _one_device(q, k, v, q_out, cache.k, page_table, kv_len, cu, q_weight, k_weight, positions,
-                                  *([rope.cos_sin, rope.axis] if rope else []))
+        self._prepare(j, _one_device(q, k, v, q_out, cache.k, page_table, kv_len, cu, q_weight, k_weight, positions,
+                                     *([rope.cos_sin, rope.axis] if rope else [])))
 
 
 class KV8Read(_Prepared):
@@ -720,7 +727,7 @@ class KV8Read(_Prepared):
                 raise ValueError("expected BF16 outputs [%d, %d, %d]" % (tokens, h.kv_heads, h.head_dim))
         j.k_out, j.v_out = _ptr(k_out), _ptr(v_out)
         self.keep = [cache, page_table, kv_len, k_out, v_out, cu]
-        self.device = _one_device(cache.k, page_table, kv_len, k_out, v_out, cu)
+        self._prepare(j, _one_device(cache.k, page_table, kv_len, k_out, v_out, cu))
 
 
 class AttnKV8(_Prepared):
@@ -746,17 +753,15 @@ class AttnKV8(_Prepared):
         if lse is not None and tuple(lse.shape) != (tokens, heads):
             raise ValueError("lse: expected [%d, %d]" % (tokens, heads))
         j.out, j.lse = _ptr(out), _ptr(lse)
-        self.device = _one_device(q, cache.k, page_table, kv_len, out, cu, lse, ws)
-        with torch.cuda.device(self.device):
+        device = _one_device(q, cache.k, page_table, kv_len, out, cu, lse, ws)
+        with torch.cuda.device(device):
             self.ws_bytes = int(load_library().convrot_attn_kv8_workspace_bytes(ctypes.byref(j)))
         if ws is None:
             # an invalid job needs none: the call says what is wrong with it
-            ws = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+            ws = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
         self.ws = ws
         self.keep = [q, cache, page_table, kv_len, out, cu, lse]
-
-    def _args(self):
-        return ctypes.byref(self.job), _ptr(self.ws), self.ws.numel() * self.ws.element_size()
+        self._prepare(j, device, _ptr(ws), ws.numel() * ws.element_size())
 
 
 def _allocating(stream, device):

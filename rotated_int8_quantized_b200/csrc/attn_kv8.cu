@@ -15,6 +15,7 @@
 // row's running maximum (whose excess over the true one is at most 2^8) is
 // lost.  Sums, maxima and accumulators are FP32.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -188,7 +189,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
     before += scan - mine;
     const long long G = min((long long)gridDim.x, total);
     const long long c = blockIdx.x;
-    if (c >= G) return;
+    if (c >= G) {
+        pdl_wait();
+        return;
+    }
     long long u = total * c / G;
     const long long u1 = total * (c + 1) / G;
     if (before <= u && u < before + mine) {
@@ -528,20 +532,21 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
         }
         u = tile_unit + unit1;
     }
+    pdl_wait();
 }
 
 // ------------------------------------------------------------ many rows a sequence
 //
 // Prompts and chunks of them: two tiles of 128 rows (of one sequence and key
 // head, rows as above) share a pass over the cache in tiles of 128 tokens, on
-// the tcgen05 tensor cores.  Thirteen warps:
+// the tcgen05 tensor cores.  Sixteen warps:
 //   0-3, 4-7  softmax of the first and second tile, a thread for each row;
 //   8-11      the cache's codes from global memory to FP16 operands in shared
 //             memory (exact), the next tile's loads in flight meanwhile;
-//   12        one thread that issues the products.
-// S = Q K^T (FP32, tensor memory) is read by the row's thread twice, once for
-// the maximum and once for the weights, which go back as FP16 over S and are
-// the first operand of P V from there.  The second product sums in tensor
+//   12-15     one thread that issues the products; the others only give their
+//             registers away: a row's thread holds a step's 128 scores.
+// S = Q K^T (FP32, tensor memory) is read by the row's thread, and the weights
+// go back as FP16 over S and are the first operand of P V from there.  The second product sums in tensor
 // memory; as its scale (the running maximum) rarely moves by 2^8, the row's
 // thread rescales it in place when it does.  While one tile is in its softmax
 // the tensor cores work on the other.
@@ -551,7 +556,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
 // there, and its barrier's phase still open to be seen, whatever the order in
 // which the warps get on: step j + 4's are written after S of step j + 2,
 // which is after every row's weights of step j + 1.
-constexpr int kPromptWarps = 13;
+constexpr int kPromptWarps = 16;
 constexpr int kPromptRows = 256;                     // two tiles
 constexpr int kKvTile = 128;
 constexpr int kInfoRing = 4;
@@ -575,6 +580,17 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// The registers of a warpgroup.  512 threads are launched with 128 each, all
+// there are; 2 x 128 x 184 + 128 x 104 + 128 x 40 are as many.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 32 columns of tensor memory, in registers when this returns (the empty
 // statements keep their uses behind the wait).
 __device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -596,6 +612,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
 
     // The tile pair of this CTA; sequence b owns the slots from floor(cu[b] group / 256) + b on.  Last ones first: under a
     // causal mask they are the longest.
+    pdl_launch_dependents();                         // attn_stream_kernel waits for this one at its end only
     const int64_t slots = gridDim.x / H;
     const int64_t slot = slots - 1 - blockIdx.x / H;
     const int h = blockIdx.x % H;
@@ -611,6 +628,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
     const int b = sm.seq;
     if (b < 0) return;
     const SeqInfo q = seq_info(S, b);
+    if (q.bad && tid == 0) report_invalid();
     const int64_t rows = (int64_t)q.n * group, row0 = (int64_t)sm.slot * kPromptRows;
     if (rows <= few_rows || row0 >= rows) return;
     const int tiles = rows - row0 > 128 ? 2 : 1;
@@ -650,6 +668,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
     const uint32_t tm_s = tmem, tm_o = tmem + 256;
 
     if (warp < 8) {
+        registers_up<184>();
         // ------------------------------------------------ a row each: queries, softmax, output
         const int t = warp >> 2, r = tid & 127;
         if (t < tiles) {
@@ -691,39 +710,40 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
             float m = -INFINITY;
             uint64_t l2 = 0;
             bool ok = true;
-            for (int j = 0; j < steps; ++j) {
-                ok = mbar_wait_bounded(info_full + 8 * (j & (kInfoRing - 1)), (j / kInfoRing) & 1, abort_flag) &&
-                     mbar_wait_bounded(s_full + 8 * t, j & 1, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            // a step's weights; Masked: some row of the warp does not see all of the tile
+            auto weigh = [&](auto masked, int j) {
+                constexpr bool Masked = decltype(masked)::value;
                 const float4 *info = sm.info[j & (kInfoRing - 1)];
                 const int limit = vis - j * kKvTile;
-                const bool masked = __any_sync(0xffffffffu, limit < kKvTile);
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, s[c]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(s[c][i]));
                 float top_t = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32];
-                    tmem_read32(ts + 32 * c, s);
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float y = -INFINITY;
-                        if (masked) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                y = fmaxf(y, 32 * c + 16 * k + i < limit ? __uint_as_float(s[16 * k + i]) : -INFINITY);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2)
-                                y = fmaxf(y, fmaxf(__uint_as_float(s[16 * k + i]), __uint_as_float(s[16 * k + i + 1])));
+                        for (int i = 0; i < 16; i += 2) {
+                            float u = __uint_as_float(s[c][16 * k + i]), v = __uint_as_float(s[c][16 * k + i + 1]);
+                            if (Masked) {
+                                u = 32 * c + 16 * k + i < limit ? u : -INFINITY;
+                                v = 32 * c + 16 * k + i + 1 < limit ? v : -INFINITY;
+                                s[c][16 * k + i] = __float_as_uint(u);
+                                s[c][16 * k + i + 1] = __float_as_uint(v);
+                            }
+                            y = fmaxf(y, fmaxf(u, v));
                         }
                         const float4 b4 = info[2 * c + k];
-                        // nothing seen in the block: -inf times a zero key scale would be NaN
+                        // a block that is not seen: -inf times a key scale of zero would be NaN
                         top_t = fmaxf(top_t, y == -INFINITY ? y : fmaf(y, f * b4.x, b4.y));
                     }
-                }
                 const bool over = top_t > m + kLazy;
                 if (__any_sync(0xffffffffu, over)) {
                     const float mn = over ? top_t : m;
@@ -733,36 +753,35 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
                     if (j > 0) {
                         // this step's S being complete, so is the product before it
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_read32(to + 32 * c, o);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(to + 16 * c, o);
+                            tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                            tmem_st_32x32b_x32(to + 32 * c, o);
+                            for (int i = 0; i < 16; ++i) {
+                                asm volatile("" : "+r"(o[i]));
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                            }
+                            tmem_st_32x32b_x16(to + 16 * c, o);
                         }
                     }
                 }
                 const float base = kPBias - (m == -INFINITY ? 0.f : m);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32], p[16];
-                    tmem_read32(ts + 32 * c, s);
+                    uint32_t p[16];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float4 b4 = info[2 * c + k];
-                        const float fb = f * b4.x, add = b4.y + base;
+                        // the smallest float instead of zero, so that a masked -inf stays -inf
+                        const float fb = Masked ? fmaxf(f * b4.x, 1.1754944e-38f) : f * b4.x, add = b4.y + base;
                         const uint64_t f2 = pack_f32x2(fb, fb), a2 = pack_f32x2(add, add);
                         uint64_t sum = 0;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint64_t d = pack_f32x2(__uint_as_float(s[16 * k + 2 * i]), __uint_as_float(s[16 * k + 2 * i + 1]));
+                            const uint64_t d = pack_f32x2(__uint_as_float(s[c][16 * k + 2 * i]), __uint_as_float(s[c][16 * k + 2 * i + 1]));
                             float u, v;
                             unpack_f32x2(fma_f32x2(d, f2, a2), u, v);
-                            if (masked) {
-                                const int col = 32 * c + 16 * k + 2 * i;
-                                u = col < limit ? u : -INFINITY;
-                                v = col + 1 < limit ? v : -INFINITY;
-                            }
                             u = ex2(u);
                             v = ex2(v);
                             sum = add_f32x2(sum, pack_f32x2(u, v));
@@ -772,6 +791,19 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
                     }
                     tmem_st_32x32b_x16(ts + 16 * c, p);
                 }
+            };
+            for (int j = 0; j < steps; ++j) {
+                ok = mbar_wait_bounded(info_full + 8 * (j & (kInfoRing - 1)), (j / kInfoRing) & 1, abort_flag) &&
+                     mbar_wait_bounded(s_full + 8 * t, j & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, vis - j * kKvTile < kKvTile))
+                    weigh(std::true_type(), j);
+                else
+                    weigh(std::false_type(), j);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(p_full + 8 * t);
@@ -806,6 +838,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
             if (in && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2;
         }
     } else if (warp < 12) {
+        registers_down<104>();
         // ------------------------------------------------ codes to operands
         // Warp w converts tokens 32 w .. + 31 of a tile: eight rows by 64 codes a step, a lane 16 codes of a row, which
         // become two of the row's 16-byte chunks; the eight lanes that store together (two rows, even and odd) fill all
@@ -887,45 +920,48 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
             if (lane == 0) mbar_arrive(v_full + 8 * st);
             load(a.c.v, a.c.vs, vx, vs);
         }
-    } else if (lane == 0 && steps > 0) {
-        // ------------------------------------------------ products
-        constexpr uint32_t idesc_s = idesc_f16(128, kKvTile, false), idesc_o = idesc_f16(128, D, true);
-        const uint32_t q_at = smem_addr(sm.q), k_at = smem_addr(sm.k), v_at = smem_addr(sm.v);
-        auto scores = [&](int t, int st) {
+    } else {
+        registers_down<40>();
+        if (warp == 12 && lane == 0 && steps > 0) {
+            // ------------------------------------------------ products
+            constexpr uint32_t idesc_s = idesc_f16(128, kKvTile, false), idesc_o = idesc_f16(128, D, true);
+            const uint32_t q_at = smem_addr(sm.q), k_at = smem_addr(sm.k), v_at = smem_addr(sm.v);
+            auto scores = [&](int t, int st) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint32_t off = (i / 4) * kBlockBytes + (i % 4) * 32;
-                umma_f16(tm_s + 128 * t, smem_desc_k_sw128(q_at + t * DB * kBlockBytes + off),
-                         smem_desc_k_sw128(k_at + st * DB * kBlockBytes + off), idesc_s, i > 0);
-            }
-            umma_commit(s_full + 8 * t);
-        };
-        bool ok = mbar_wait_bounded(q_full, 0, abort_flag) && mbar_wait_bounded(k_full, 0, abort_flag);
-        tc_fence_after();
-        if (ok) {
-            for (int t = 0; t < tiles; ++t) scores(t, 0);
-            if (steps > 2) umma_commit(k_empty);         // waited for by the stage's next use, where there is one
-        }
-        for (int j = 0; ok && j < steps; ++j) {
-            const int st = j & 1, sn = st ^ 1;
-            ok = mbar_wait_bounded(v_full + 8 * st, (j >> 1) & 1, abort_flag);
-            if (ok && j + 1 < steps) ok = mbar_wait_bounded(k_full + 8 * sn, ((j + 1) >> 1) & 1, abort_flag);
-            for (int t = 0; ok && t < tiles; ++t) {
-                ok = mbar_wait_bounded(p_full + 8 * t, j & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < kKvTile / 16; ++i)
-                    umma_f16_ts(tm_o + D * t, tm_s + 128 * t + 8 * i,
-                                smem_desc_mn_sw128(v_at + st * DB * kBlockBytes + i * 2048, kBlockBytes), idesc_o, j > 0 || i > 0);
-                if (j + 1 < steps)
-                    scores(t, sn);
-                else
-                    umma_commit(o_full + 8 * t);
-            }
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t off = (i / 4) * kBlockBytes + (i % 4) * 32;
+                    umma_f16(tm_s + 128 * t, smem_desc_k_sw128(q_at + t * DB * kBlockBytes + off),
+                             smem_desc_k_sw128(k_at + st * DB * kBlockBytes + off), idesc_s, i > 0);
+                }
+                umma_commit(s_full + 8 * t);
+            };
+            bool ok = mbar_wait_bounded(q_full, 0, abort_flag) && mbar_wait_bounded(k_full, 0, abort_flag);
+            tc_fence_after();
             if (ok) {
-                if (j + 2 < steps) umma_commit(v_empty + 8 * st);
-                if (j + 3 < steps) umma_commit(k_empty + 8 * sn);
+                for (int t = 0; t < tiles; ++t) scores(t, 0);
+                if (steps > 2) umma_commit(k_empty);         // waited for by the stage's next use, where there is one
+            }
+            for (int j = 0; ok && j < steps; ++j) {
+                const int st = j & 1, sn = st ^ 1;
+                ok = mbar_wait_bounded(v_full + 8 * st, (j >> 1) & 1, abort_flag);
+                if (ok && j + 1 < steps) ok = mbar_wait_bounded(k_full + 8 * sn, ((j + 1) >> 1) & 1, abort_flag);
+                for (int t = 0; ok && t < tiles; ++t) {
+                    ok = mbar_wait_bounded(p_full + 8 * t, j & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < kKvTile / 16; ++i)
+                        umma_f16_ts(tm_o + D * t, tm_s + 128 * t + 8 * i,
+                                    smem_desc_mn_sw128(v_at + st * DB * kBlockBytes + i * 2048, kBlockBytes), idesc_o, j > 0 || i > 0);
+                    if (j + 1 < steps)
+                        scores(t, sn);
+                    else
+                        umma_commit(o_full + 8 * t);
+                }
+                if (ok) {
+                    if (j + 2 < steps) umma_commit(v_empty + 8 * st);
+                    if (j + 3 < steps) umma_commit(k_empty + 8 * sn);
+                }
             }
         }
     }
@@ -958,35 +994,64 @@ int64_t attn_kv8_workspace_bytes(int64_t tokens, int32_t batch, int32_t q_heads,
     return ((grid + 63) / 64 * 64 + 2 * grid * rows * (dim + 2)) * 4;
 }
 
+// Shared memory beyond the default, set once for a kernel and device.
+template <typename Kernel>
+static cudaError_t allow_smem(Kernel *kernel, int bytes, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+}
+
+// beside: launched behind attn_prompt_kernel and independent of it, so it may
+// start while that one's last CTAs run (it ends after them: a kernel that
+// follows on the stream finds both complete).
 template <int D, int NT>
-static cudaError_t launch_stream(const AttnArgs &a, int sms, cudaStream_t stream) {
+static cudaError_t launch_stream(const AttnArgs &a, int few_rows, int sms, bool beside, cudaStream_t stream) {
+    static bool done[64] = {};
     const int bytes = (int)sizeof(StreamSmem<D, NT>);
-    cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = allow_smem(attn_stream_kernel<D, NT>, bytes, done);
     if (e != cudaSuccess) return e;
-    attn_stream_kernel<D, NT><<<sms * stream_ctas(NT), kStreamWarps * 32, bytes, stream>>>(a, kFewRows);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(sms * stream_ctas(NT)));
+    cfg.blockDim = dim3(kStreamWarps * 32);
+    cfg.dynamicSmemBytes = (size_t)bytes;
+    cfg.stream = stream;
+    cfg.attrs = beside ? attr : nullptr;
+    cfg.numAttrs = beside ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attn_stream_kernel<D, NT>, a, few_rows);
 }
 
 template <int D>
-static cudaError_t launch_prompt(const AttnArgs &a, cudaStream_t stream) {
+static cudaError_t launch_prompt(const AttnArgs &a, int few_rows, cudaStream_t stream) {
+    static bool done[64] = {};
     const int bytes = (int)sizeof(PromptSmem<D>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = allow_smem(attn_prompt_kernel<D>, bytes, done);
     if (e != cudaSuccess) return e;
     const int64_t slots = a.s.tokens * (a.q_heads / a.c.heads) / kPromptRows + a.s.batch;
-    attn_prompt_kernel<D><<<(unsigned)(slots * a.c.heads), kPromptWarps * 32, bytes, stream>>>(a, kFewRows);
+    attn_prompt_kernel<D><<<(unsigned)(slots * a.c.heads), kPromptWarps * 32, bytes, stream>>>(a, few_rows);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_kv8(const AttnArgs &a, int sms, cudaStream_t stream) {
-    // a sequence with more rows can only be there if the step has them
-    const int64_t most = a.s.cu ? a.s.tokens : 1;
-    if (most * (a.q_heads / a.c.heads) > kFewRows) {
-        const cudaError_t e = a.c.dim == 128 ? launch_prompt<128>(a, stream) : launch_prompt<64>(a, stream);
-        if (e != cudaSuccess) return e;
+    // Which kernel a sequence takes is decided by its rows, on the device; what the host can tell is the most rows that
+    // one may have, and for a single sequence that they are all the step has.
+    const int64_t most = (a.s.cu ? a.s.tokens : 1) * (a.q_heads / a.c.heads);
+    const bool prompts = most > kFewRows;
+    const int few_rows = prompts && a.s.batch == 1 ? -1 : kFewRows;
+    if (prompts) {
+        const cudaError_t e = a.c.dim == 128 ? launch_prompt<128>(a, few_rows, stream) : launch_prompt<64>(a, few_rows, stream);
+        if (e != cudaSuccess || few_rows < 0) return e;
     }
     const int nt = stream_tiles(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
-    if (a.c.dim == 128) return nt == 1 ? launch_stream<128, 1>(a, sms, stream) : launch_stream<128, 2>(a, sms, stream);
-    return nt == 1 ? launch_stream<64, 1>(a, sms, stream) : launch_stream<64, 2>(a, sms, stream);
+    if (a.c.dim == 128)
+        return nt == 1 ? launch_stream<128, 1>(a, kFewRows, sms, prompts, stream) : launch_stream<128, 2>(a, kFewRows, sms, prompts, stream);
+    return nt == 1 ? launch_stream<64, 1>(a, kFewRows, sms, prompts, stream) : launch_stream<64, 2>(a, kFewRows, sms, prompts, stream);
 }
 
 }  // namespace convrot
