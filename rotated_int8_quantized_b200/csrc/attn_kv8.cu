@@ -11,9 +11,10 @@
 // power of two per row that brings the row's largest element to [2^14, 2^15):
 // exact for every element above 2^-28 of the largest, off by 2^-39 of the
 // largest below that (a BF16 product would be no closer).  p' is held as FP16
-// scaled by 2^7: 11 bits where BF16 keeps 8, and nothing above 2^-31 of the
-// row's running maximum (whose excess over the true one is at most 2^8) is
-// lost.  Sums, maxima and accumulators are FP32.
+// scaled by 2^4: 11 bits where BF16 keeps 8, nothing above 2^-29 of the row's
+// maximum lost, and room for 2^11 more, so that the running maximum (and with
+// it all that was summed under it) is moved only when it falls that far behind.
+// Sums, maxima and accumulators are FP32.
 #include <cstdint>
 #include <type_traits>
 #include <cuda_bf16.h>
@@ -27,8 +28,8 @@ namespace convrot {
 
 constexpr int kStreamWarps = 4;
 constexpr int kStreamUnit = 16 * kStreamWarps;      // tokens a CTA takes at a time: a block for each warp
-constexpr float kPBias = 7.f;                       // p' is held times 2^7
-constexpr float kLazy = 8.f;                        // the running maximum moves once it is exceeded by 2^8
+constexpr float kPBias = 4.f;                       // p' is held times 2^4
+constexpr float kLazy = 11.f;                       // the running maximum moves once it is exceeded by 2^11
 // Sequences with at most so many rows (tokens times queries a key head) are
 // streamed, longer ones go through the tensor-core tiles.
 constexpr int kFewRows = 64;
@@ -710,86 +711,135 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
             float m = -INFINITY;
             uint64_t l2 = 0;
             bool ok = true;
-            // a step's weights; Masked: some row of the warp does not see all of the tile
+            // A step's weights, 32 columns at a time, the next 32 scores on their way.  Masked: some row of the warp does
+            // not see all of the tile.  The weights are taken against the maximum so far without looking at the scores
+            // first: were one far above it, their sum says so (beyond 2^15; 32 weights of 2^kPBias at a maximum that
+            // holds reach 2^9), and these 32 are done again against their own maximum, what the row has already scaled
+            // to it.  By this row alone: what a row gets does not depend on its neighbours.
             auto weigh = [&](auto masked, int j) {
                 constexpr bool Masked = decltype(masked)::value;
                 const float4 *info = sm.info[j & (kInfoRing - 1)];
                 const int limit = vis - j * kKvTile;
-                uint32_t s[4][32];
+                auto mask = [&](uint32_t (&s)[32], int c) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, s[c]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(s[c][i]));
-                float top_t = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int i = 0; i < 32; ++i) {
+                        asm volatile("" : "+r"(s[i]));                              // behind the wait
+                        if (Masked && i >= limit - 32 * c) s[i] = 0xFF800000u;      // -inf
+                    }
+                };
+                auto maximum = [&](const uint32_t (&s)[32], int c) {
+                    float top = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float y = -INFINITY;
+                        float y[4];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float u = __uint_as_float(s[c][16 * k + i]), v = __uint_as_float(s[c][16 * k + i + 1]);
-                            if (Masked) {
-                                u = 32 * c + 16 * k + i < limit ? u : -INFINITY;
-                                v = 32 * c + 16 * k + i + 1 < limit ? v : -INFINITY;
-                                s[c][16 * k + i] = __float_as_uint(u);
-                                s[c][16 * k + i + 1] = __float_as_uint(v);
-                            }
-                            y = fmaxf(y, fmaxf(u, v));
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = __uint_as_float(s[16 * k + i]);
+                            y[i & 3] = i < 4 ? x : fmaxf(y[i & 3], x);
                         }
+                        const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
                         const float4 b4 = info[2 * c + k];
                         // a block that is not seen: -inf times a key scale of zero would be NaN
-                        top_t = fmaxf(top_t, y == -INFINITY ? y : fmaf(y, f * b4.x, b4.y));
+                        top = fmaxf(top, z == -INFINITY ? z : fmaf(z, f * b4.x, b4.y));
                     }
-                const bool over = top_t > m + kLazy;
-                if (__any_sync(0xffffffffu, over)) {
-                    const float mn = over ? top_t : m;
-                    const float al = m == mn ? 1.f : ex2(m - mn);
-                    m = mn;
-                    l2 = mul_f32x2(l2, pack_f32x2(al, al));
-                    if (j > 0) {
-                        // this step's S being complete, so is the product before it
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b_x16(to + 16 * c, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                asm volatile("" : "+r"(o[i]));
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                            }
-                            tmem_st_32x32b_x16(to + 16 * c, o);
-                        }
-                    }
-                }
-                const float base = kPBias - (m == -INFINITY ? 0.f : m);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
+                    return top;
+                };
+                auto weights = [&](const uint32_t (&s)[32], int c, uint32_t (&p)[16], uint64_t &l_add) {
+                    const float base = kPBias - (m == -INFINITY ? 0.f : m);
+                    uint64_t sum[4];
+                    float scale[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float4 b4 = info[2 * c + k];
                         // the smallest float instead of zero, so that a masked -inf stays -inf
                         const float fb = Masked ? fmaxf(f * b4.x, 1.1754944e-38f) : f * b4.x, add = b4.y + base;
                         const uint64_t f2 = pack_f32x2(fb, fb), a2 = pack_f32x2(add, add);
-                        uint64_t sum = 0;
+                        scale[k] = b4.z;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint64_t d = pack_f32x2(__uint_as_float(s[c][16 * k + 2 * i]), __uint_as_float(s[c][16 * k + 2 * i + 1]));
+                            const uint64_t d = pack_f32x2(__uint_as_float(s[16 * k + 2 * i]), __uint_as_float(s[16 * k + 2 * i + 1]));
                             float u, v;
                             unpack_f32x2(fma_f32x2(d, f2, a2), u, v);
                             u = ex2(u);
                             v = ex2(v);
-                            sum = add_f32x2(sum, pack_f32x2(u, v));
+                            const uint64_t uv = pack_f32x2(u, v);
+                            sum[2 * k + (i & 1)] = i < 2 ? uv : add_f32x2(sum[2 * k + (i & 1)], uv);
                             p[8 * k + i] = pack_half2(u, v);
                         }
-                        l2 = fma_f32x2(sum, pack_f32x2(b4.z, b4.z), l2);
                     }
+                    const uint64_t s0 = add_f32x2(sum[0], sum[1]), s1 = add_f32x2(sum[2], sum[3]);
+                    l_add = fma_f32x2(s0, pack_f32x2(scale[0], scale[0]), mul_f32x2(s1, pack_f32x2(scale[1], scale[1])));
+                    float u, v;
+                    unpack_f32x2(add_f32x2(s0, s1), u, v);
+                    return u + v;
+                };
+                auto chunk = [&](const uint32_t (&s)[32], int c) {
+                    uint32_t p[16];
+                    uint64_t l_add;
+                    const bool over = weights(s, c, p, l_add) > 32768.f;
+                    if (__any_sync(0xffffffffu, over)) {
+                        const float mn = over ? maximum(s, c) : m;
+                        const float al = over ? ex2(m - mn) : 1.f;
+                        m = mn;
+                        l2 = mul_f32x2(l2, pack_f32x2(al, al));
+                        // the sums so far (this step's S being complete, so is the product before it) ..
+#pragma unroll 1
+                        for (int i = 0; j > 0 && i < D / 16; ++i) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(to + 16 * i, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                asm volatile("" : "+r"(o[k]));
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                            }
+                            tmem_st_32x32b_x16(to + 16 * i, o);
+                        }
+                        // .. and this step's weights so far
+                        tmem_st_wait();
+#pragma unroll 1
+                        for (int i = 0; i < c; ++i) {
+                            tmem_ld_32x32b_x16(ts + 16 * i, p);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                asm volatile("" : "+r"(p[k]));
+                                const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&p[k]));
+                                p[k] = pack_half2(w.x * al, w.y * al);
+                            }
+                            tmem_st_32x32b_x16(ts + 16 * i, p);
+                        }
+                        weights(s, c, p, l_add);
+                    }
+                    l2 = add_f32x2(l2, l_add);
                     tmem_st_32x32b_x16(ts + 16 * c, p);
+                };
+                uint32_t s0[32], s1[32];
+                if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                    // no maximum yet (the first step, or nothing seen so far): the step's own, nothing to scale to it
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_32x32b_x32(ts + 32 * c, s0);
+                        tmem_ld_wait();
+                        mask(s0, c);
+                        top = fmaxf(top, maximum(s0, c));
+                    }
+                    if (m == -INFINITY) m = top;
+                }
+                tmem_ld_32x32b_x32(ts, s0);
+                tmem_ld_wait();
+                mask(s0, 0);
+#pragma unroll 1
+                for (int c = 0; c < 4; c += 2) {
+                    tmem_ld_32x32b_x32(ts + 32 * (c + 1), s1);
+                    chunk(s0, c);
+                    tmem_ld_wait();
+                    mask(s1, c + 1);
+                    if (c < 2) tmem_ld_32x32b_x32(ts + 32 * (c + 2), s0);
+                    chunk(s1, c + 1);
+                    tmem_ld_wait();
+                    if (c < 2) mask(s0, c + 2);
                 }
             };
             for (int j = 0; j < steps; ++j) {

@@ -300,16 +300,17 @@ def _check_attention(paged, q, out, lse, news, causal, scale, rows=None):
     weight and the weights' sum by that much each; the result is rounded to BF16 (2^-8).  lse: the score's error and
     FP32 roundings of a sum of weights and of the logarithm.
 
-    FP16 ends at 2^-24, and a weight (times its value scale) is held as 2^7 of its share of the running maximum, so
-    each is off by up to half of 2^-24 / 2^7 of that maximum, which is at most the sequence's largest value scale; a
-    code is at most 127 and the weights' sum at least 1: 2^-32 * 127 * tokens * largest scale in all."""
+    FP16 ends at 2^-24, and a weight (times its value scale) is held as 2^4 of its share of the running maximum, so
+    each is off by up to half of 2^-24 / 2^4 of that maximum, which is at most the sequence's largest value scale; a
+    code is at most 127 and the weights' sum at least 1: 2^-29 * 127 * tokens * largest scale in all.  (Where a later
+    token moves the maximum, a weight already rounded is rounded again: 2^-11 counts both.)"""
     t = 0
     o, z = bits_to_f64(out), lse.cpu().numpy().astype(np.float64)
     qf = bits_to_f64(q)
     for b, n in enumerate(news):
         k, v = paged.values(b, 0), paged.values(b, 1)
         used = paged.table.numpy()[b][:-(-paged.lens[b] // paged.page)]
-        lost = 2.0 ** -32 * 127 * paged.lens[b] * np.nanmax(paged.cache.v_scale.cpu().numpy()[used], initial=0)
+        lost = 2.0 ** -29 * 127 * paged.lens[b] * np.nanmax(paged.cache.v_scale.cpu().numpy()[used], initial=0)
         pick = range(n) if rows is None or n <= rows else sorted(set(np.linspace(0, n - 1, rows).astype(int)))
         for i in pick:
             # row i alone: a causal row sees len - n + i + 1 tokens
