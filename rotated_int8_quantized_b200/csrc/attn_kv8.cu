@@ -581,6 +581,17 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// True in one lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // The registers of a warpgroup.  512 threads are launched with 128 each, all
 // there are; 2 x 128 x 184 + 128 x 104 + 128 x 40 are as many.
 template <int N>
@@ -665,7 +676,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *(volatile uint32_t *)&sm.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *(volatile uint32_t *)&sm.tmem, 0);
     const uint32_t tm_s = tmem, tm_o = tmem + 256;
 
     if (warp < 8) {
@@ -972,57 +983,75 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
         }
     } else {
         registers_down<40>();
-        if (warp == 12 && lane == 0 && steps > 0) {
+        if (warp == 12 && steps > 0) {
             // ------------------------------------------------ products
+            // The whole warp goes through the loop and one lane issues: what the instructions take (descriptors, addresses)
+            // is then the same for the warp and stays in uniform registers.
             constexpr uint32_t idesc_s = idesc_f16(128, kKvTile, false), idesc_o = idesc_f16(128, D, true);
-            const uint32_t q_at = smem_addr(sm.q), k_at = smem_addr(sm.k), v_at = smem_addr(sm.v);
+            // operands' addresses count in 16 bytes in their descriptors' low bits
+            constexpr uint32_t kStage = DB * kBlockBytes / 16;
+            const uint64_t q_desc = smem_desc_k_sw128(smem_addr(sm.q)), k_desc = smem_desc_k_sw128(smem_addr(sm.k)),
+                           v_desc = smem_desc_mn_sw128(smem_addr(sm.v), kBlockBytes);
+            const bool one = elect_one();
             auto scores = [&](int t, int st) {
+                const uint64_t qd = q_desc + t * kStage, kd = k_desc + st * kStage;
+                const uint32_t d = tm_s + 128 * t;
+                if (one) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = (i / 4) * kBlockBytes + (i % 4) * 32;
-                    umma_f16(tm_s + 128 * t, smem_desc_k_sw128(q_at + t * DB * kBlockBytes + off),
-                             smem_desc_k_sw128(k_at + st * DB * kBlockBytes + off), idesc_s, i > 0);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t off = ((i / 4) * kBlockBytes + (i % 4) * 32) / 16;
+                        umma_f16(d, qd + off, kd + off, idesc_s, i > 0);
+                    }
+                    umma_commit(s_full + 8 * t);
                 }
-                umma_commit(s_full + 8 * t);
+            };
+            auto values = [&](int t, int st, bool first, bool last) {
+                const uint64_t vd = v_desc + st * kStage;
+                const uint32_t d = tm_o + D * t, p = tm_s + 128 * t;
+                if (one) {
+                    umma_f16_ts(d, p, vd, idesc_o, !first);
+#pragma unroll
+                    for (int i = 1; i < kKvTile / 16; ++i) umma_f16_ts(d, p + 8 * i, vd + i * (16 * 128 / 16), idesc_o, 1);
+                    if (last) umma_commit(o_full + 8 * t);
+                }
             };
             bool ok = mbar_wait_bounded(q_full, 0, abort_flag) && mbar_wait_bounded(k_full, 0, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             if (ok) {
-                for (int t = 0; t < tiles; ++t) scores(t, 0);
-                if (steps > 2) umma_commit(k_empty);         // waited for by the stage's next use, where there is one
+                scores(0, 0);
+                if (tiles > 1) scores(1, 0);
+                if (one && steps > 2) umma_commit(k_empty);      // waited for by the stage's next use, where there is one
             }
             for (int j = 0; ok && j < steps; ++j) {
                 const int st = j & 1, sn = st ^ 1;
                 ok = mbar_wait_bounded(v_full + 8 * st, (j >> 1) & 1, abort_flag);
                 if (ok && j + 1 < steps) ok = mbar_wait_bounded(k_full + 8 * sn, ((j + 1) >> 1) & 1, abort_flag);
-                for (int t = 0; ok && t < tiles; ++t) {
-                    ok = mbar_wait_bounded(p_full + 8 * t, j & 1, abort_flag);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t == 1 && tiles < 2) break;
+                    if (ok) ok = mbar_wait_bounded(p_full + 8 * t, j & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < kKvTile / 16; ++i)
-                        umma_f16_ts(tm_o + D * t, tm_s + 128 * t + 8 * i,
-                                    smem_desc_mn_sw128(v_at + st * DB * kBlockBytes + i * 2048, kBlockBytes), idesc_o, j > 0 || i > 0);
-                    if (j + 1 < steps)
-                        scores(t, sn);
-                    else
-                        umma_commit(o_full + 8 * t);
+                    values(t, st, j == 0, j + 1 == steps);
+                    if (j + 1 < steps) scores(t, sn);
                 }
-                if (ok) {
+                if (ok && one) {
                     if (j + 2 < steps) umma_commit(v_empty + 8 * st);
                     if (j + 3 < steps) umma_commit(k_empty + 8 * sn);
                 }
             }
+            if (one && *abort_flag) {
+                // given up: what was issued still has to be complete before tensor memory goes (otherwise the rows' threads
+                // have waited for the last products)
+                umma_commit(drain);
+                const unsigned long long start = global_timer_ns();
+                while (!mbar_try_wait(drain, 0) && global_timer_ns() - start < 1000000000ull) {}
+            }
+            __syncwarp();
         }
     }
-    // Every product is complete before tensor memory goes: the rows' threads waited for the last ones; a run that gave
-    // up waits here for what it had issued.
-    if (warp == 12 && lane == 0 && *abort_flag) {
-        umma_commit(drain);
-        const unsigned long long start = global_timer_ns();
-        while (!mbar_try_wait(drain, 0) && global_timer_ns() - start < 1000000000ull) {}
-    }
-    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 12) {
