@@ -592,6 +592,28 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Instructions that stay in the order written (volatile).
+__device__ __forceinline__ float in_order_ex2(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t in_order_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t in_order_add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm volatile("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t in_order_half2(float lo, float hi) {
+    uint32_t d;
+    asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 // The registers of a warpgroup.  512 threads are launched with 128 each, all
 // there are; 2 x 128 x 184 + 128 x 104 + 128 x 40 are as many.
 template <int N>
@@ -722,149 +744,130 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
             float m = -INFINITY;
             uint64_t l2 = 0;
             bool ok = true;
-            // A step's weights, 32 columns at a time, the next 32 scores on their way.  Masked: some row of the warp does
-            // not see all of the tile.  The weights are taken against the maximum so far without looking at the scores
-            // first: were one far above it, their sum says so (beyond 2^15; 32 weights of 2^kPBias at a maximum that
-            // holds reach 2^9), and these 32 are done again against their own maximum, what the row has already scaled
-            // to it.  By this row alone: what a row gets does not depend on its neighbours.
-            auto weigh = [&](auto masked, int j) {
-                constexpr bool Masked = decltype(masked)::value;
-                const float4 *info = sm.info[j & (kInfoRing - 1)];
-                const int limit = vis - j * kKvTile;
-                auto mask = [&](uint32_t (&s)[32], int c) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        asm volatile("" : "+r"(s[i]));                              // behind the wait
-                        if (Masked && i >= limit - 32 * c) s[i] = 0xFF800000u;      // -inf
-                    }
-                };
-                auto maximum = [&](const uint32_t (&s)[32], int c) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float y[4];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = __uint_as_float(s[16 * k + i]);
-                            y[i & 3] = i < 4 ? x : fmaxf(y[i & 3], x);
-                        }
-                        const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                        const float4 b4 = info[2 * c + k];
-                        // a block that is not seen: -inf times a key scale of zero would be NaN
-                        top = fmaxf(top, z == -INFINITY ? z : fmaf(z, f * b4.x, b4.y));
-                    }
-                    return top;
-                };
-                auto weights = [&](const uint32_t (&s)[32], int c, uint32_t (&p)[16], uint64_t &l_add) {
-                    const float base = kPBias - (m == -INFINITY ? 0.f : m);
-                    uint64_t sum[4];
-                    float scale[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float4 b4 = info[2 * c + k];
-                        // the smallest float instead of zero, so that a masked -inf stays -inf
-                        const float fb = Masked ? fmaxf(f * b4.x, 1.1754944e-38f) : f * b4.x, add = b4.y + base;
-                        const uint64_t f2 = pack_f32x2(fb, fb), a2 = pack_f32x2(add, add);
-                        scale[k] = b4.z;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint64_t d = pack_f32x2(__uint_as_float(s[16 * k + 2 * i]), __uint_as_float(s[16 * k + 2 * i + 1]));
-                            float u, v;
-                            unpack_f32x2(fma_f32x2(d, f2, a2), u, v);
-                            u = ex2(u);
-                            v = ex2(v);
-                            const uint64_t uv = pack_f32x2(u, v);
-                            sum[2 * k + (i & 1)] = i < 2 ? uv : add_f32x2(sum[2 * k + (i & 1)], uv);
-                            p[8 * k + i] = pack_half2(u, v);
-                        }
-                    }
-                    const uint64_t s0 = add_f32x2(sum[0], sum[1]), s1 = add_f32x2(sum[2], sum[3]);
-                    l_add = fma_f32x2(s0, pack_f32x2(scale[0], scale[0]), mul_f32x2(s1, pack_f32x2(scale[1], scale[1])));
-                    float u, v;
-                    unpack_f32x2(add_f32x2(s0, s1), u, v);
-                    return u + v;
-                };
-                auto chunk = [&](const uint32_t (&s)[32], int c) {
-                    uint32_t p[16];
-                    uint64_t l_add;
-                    const bool over = weights(s, c, p, l_add) > 32768.f;
-                    if (__any_sync(0xffffffffu, over)) {
-                        const float mn = over ? maximum(s, c) : m;
-                        const float al = over ? ex2(m - mn) : 1.f;
-                        m = mn;
-                        l2 = mul_f32x2(l2, pack_f32x2(al, al));
-                        // the sums so far (this step's S being complete, so is the product before it) ..
-#pragma unroll 1
-                        for (int i = 0; j > 0 && i < D / 16; ++i) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b_x16(to + 16 * i, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                asm volatile("" : "+r"(o[k]));
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                            }
-                            tmem_st_32x32b_x16(to + 16 * i, o);
-                        }
-                        // .. and this step's weights so far
-                        tmem_st_wait();
-#pragma unroll 1
-                        for (int i = 0; i < c; ++i) {
-                            tmem_ld_32x32b_x16(ts + 16 * i, p);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                asm volatile("" : "+r"(p[k]));
-                                const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&p[k]));
-                                p[k] = pack_half2(w.x * al, w.y * al);
-                            }
-                            tmem_st_32x32b_x16(ts + 16 * i, p);
-                        }
-                        weights(s, c, p, l_add);
-                    }
-                    l2 = add_f32x2(l2, l_add);
-                    tmem_st_32x32b_x16(ts + 16 * c, p);
-                };
-                uint32_t s0[32], s1[32];
-                if (__any_sync(0xffffffffu, m == -INFINITY)) {
-                    // no maximum yet (the first step, or nothing seen so far): the step's own, nothing to scale to it
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld_32x32b_x32(ts + 32 * c, s0);
-                        tmem_ld_wait();
-                        mask(s0, c);
-                        top = fmaxf(top, maximum(s0, c));
-                    }
-                    if (m == -INFINITY) m = top;
-                }
-                tmem_ld_32x32b_x32(ts, s0);
-                tmem_ld_wait();
-                mask(s0, 0);
-#pragma unroll 1
-                for (int c = 0; c < 4; c += 2) {
-                    tmem_ld_32x32b_x32(ts + 32 * (c + 1), s1);
-                    chunk(s0, c);
-                    tmem_ld_wait();
-                    mask(s1, c + 1);
-                    if (c < 2) tmem_ld_32x32b_x32(ts + 32 * (c + 2), s0);
-                    chunk(s1, c + 1);
-                    tmem_ld_wait();
-                    if (c < 2) mask(s0, c + 2);
-                }
-            };
             for (int j = 0; j < steps; ++j) {
-                ok = mbar_wait_bounded(info_full + 8 * (j & (kInfoRing - 1)), (j / kInfoRing) & 1, abort_flag) &&
-                     mbar_wait_bounded(s_full + 8 * t, j & 1, abort_flag);
+                // the blocks' scales, on their way while S is computed
+                ok = mbar_wait_bounded(info_full + 8 * (j & (kInfoRing - 1)), (j / kInfoRing) & 1, abort_flag);
+                float fb[8], lv[8], iv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 b4 = sm.info[j & (kInfoRing - 1)][i];
+                    fb[i] = f * b4.x;
+                    lv[i] = b4.y;
+                    iv[i] = b4.z;
+                }
+                ok = ok && mbar_wait_bounded(s_full + 8 * t, j & 1, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (__any_sync(0xffffffffu, vis - j * kKvTile < kKvTile))
-                    weigh(std::true_type(), j);
-                else
-                    weigh(std::false_type(), j);
+                const int limit = vis - j * kKvTile;
+                const bool masked = __any_sync(0xffffffffu, limit < kKvTile);       // some row does not see all of the tile
+                auto ready = [&](uint32_t (&s)[32], int c) {
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(s[i]));     // behind the wait
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i >= limit - 32 * c) s[i] = 0xFF800000u;            // -inf
+                    }
+                };
+                uint32_t s[2][32], p[4][16];
+                // The weights are taken against the maximum so far without looking at the scores first: were one far above
+                // it, their sum says so (beyond 2^15; 128 weights of 2^kPBias at a maximum that holds reach 2^11), and
+                // the step is done again against the scores' own maximum.  By this row alone: what a row gets does not
+                // depend on its neighbours.
+                bool over = m == -INFINITY;          // the first step, or nothing seen so far
+                uint64_t l_add = 0;
+                for (int turn = 0;; ++turn) {
+                    if (__any_sync(0xffffffffu, over)) {
+                        float top = -INFINITY;
+                        tmem_ld_32x32b_x32(ts, s[0]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            ready(s[c & 1], c);
+                            if (c < 3) tmem_ld_32x32b_x32(ts + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float y[4];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float x = __uint_as_float(s[c & 1][16 * k + i]);
+                                    y[i & 3] = i < 4 ? x : fmaxf(y[i & 3], x);
+                                }
+                                const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                                // a block that is not seen: -inf times a key scale of zero would be NaN
+                                top = fmaxf(top, z == -INFINITY ? z : fmaf(z, fb[2 * c + k], lv[2 * c + k]));
+                            }
+                        }
+                        const float mn = over ? top : m;
+                        const float al = m == mn ? 1.f : ex2(m - mn);
+                        m = mn;
+                        l2 = mul_f32x2(l2, pack_f32x2(al, al));
+                        if (j > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+                            // what was summed so far: this step's S being complete, so is the product before it
+#pragma unroll 1
+                            for (int i = 0; i < D / 32; ++i) {
+                                tmem_read32(to + 32 * i, s[0]);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) s[0][k] = __float_as_uint(__uint_as_float(s[0][k]) * al);
+                                tmem_st_32x32b_x32(to + 32 * i, s[0]);
+                            }
+                        }
+                    }
+                    // Two columns at a time, in the order written: the exponentials are what bounds a row (8 clocks a warp
+                    // and instruction), so the product of the next pair and the sum and packing of the pair before last
+                    // stand between them.
+                    const float base = kPBias - (m == -INFINITY ? 0.f : m);
+                    uint64_t all = 0, sum[2], x[2], f2, a2;
+                    float u[3], v[3];
+                    l_add = 0;
+                    tmem_ld_32x32b_x32(ts, s[0]);
+#pragma unroll
+                    for (int n = 0; n < 64 + 3; ++n) {
+                        if (n < 64) {
+                            if (n % 16 == 0) {
+                                ready(s[n / 16 & 1], n / 16);
+                                if (n < 48) tmem_ld_32x32b_x32(ts + 2 * n + 32, s[(n / 16 & 1) ^ 1]);
+                            }
+                            if (n % 8 == 0) {
+                                // the smallest float instead of zero, so that a masked -inf stays -inf
+                                const float fk = fmaxf(fb[n / 8], 1.1754944e-38f), ak = lv[n / 8] + base;
+                                f2 = pack_f32x2(fk, fk);
+                                a2 = pack_f32x2(ak, ak);
+                            }
+                            const uint32_t *d = s[n / 16 & 1] + 2 * (n % 16);
+                            x[n & 1] = in_order_fma2(pack_f32x2(__uint_as_float(d[0]), __uint_as_float(d[1])), f2, a2);
+                        }
+                        if (n >= 1 && n < 65) {
+                            float lo, hi;
+                            unpack_f32x2(x[(n - 1) & 1], lo, hi);
+                            u[(n - 1) % 3] = in_order_ex2(lo);
+                            v[(n - 1) % 3] = in_order_ex2(hi);
+                        }
+                        if (n >= 3) {
+                            const int q = n - 3;
+                            const uint64_t uv = pack_f32x2(u[q % 3], v[q % 3]);
+                            sum[q & 1] = q % 8 < 2 ? uv : in_order_add2(sum[q & 1], uv);
+                            p[q / 16][q % 16] = in_order_half2(u[q % 3], v[q % 3]);
+                            if (q % 8 == 7) {
+                                const uint64_t block = in_order_add2(sum[0], sum[1]);
+                                all = in_order_add2(all, block);
+                                l_add = in_order_fma2(block, pack_f32x2(iv[q / 8], iv[q / 8]), l_add);
+                            }
+                        }
+                    }
+                    float lo, hi;
+                    unpack_f32x2(all, lo, hi);
+                    over = lo + hi > 32768.f;
+                    // sums against the scores' own maximum stay small (and where scores are so large that FP32 no longer
+                    // tells them apart, twice is enough)
+                    if (turn == 2 || !__any_sync(0xffffffffu, over)) break;
+                }
+                l2 = add_f32x2(l2, l_add);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_st_32x32b_x16(ts + 16 * c, p[c]);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(p_full + 8 * t);
