@@ -28,6 +28,7 @@ namespace convrot {
 
 constexpr int kStreamWarps = 4;
 constexpr int kStreamUnit = 16 * kStreamWarps;      // tokens a CTA takes at a time: a block for each warp
+constexpr int kJoin = 64;                           // parts of a tile joined at a time
 constexpr float kPBias = 4.f;                       // p' is held times 2^4
 constexpr float kLazy = 11.f;                       // the running maximum moves once it is exceeded by 2^11
 // Sequences with at most so many rows (tokens times queries a key head) are
@@ -91,6 +92,12 @@ __device__ __forceinline__ uint2 ld_stream8(const void *p) {
 
 // Rows, cached tokens and first row of sequence b, held to the step's bounds
 // whatever the device arrays say.
+// a / b for a >= 0 and b > 0, in 32 bits where they do (a 64-bit quotient is a
+// quarter of a microsecond, and several stand between a small call and its end).
+__device__ __forceinline__ long long quotient(long long a, int b) {
+    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 struct SeqInfo {
     int64_t t0;
     int n, len;
@@ -134,7 +141,7 @@ __device__ __forceinline__ SeqInfo seq_info(const KvSeqs &s, int b) {
 // the counter back to zero.
 template <int D, int NT>
 struct StreamSmem {
-    float o[kStreamWarps][8 * NT][D + 4];
+    float o[kStreamWarps][8 * NT][D + 4];            // later the maxima and sums of a tile's parts, [kJoin][8 NT][2]
     float m[kStreamWarps][8 * NT], l[kStreamWarps][8 * NT];
     long long first[kStreamWarps];
     int seq, last;
@@ -142,7 +149,7 @@ struct StreamSmem {
 };
 
 // CTAs of the persistent grid on an SM; also what the registers are held to.
-constexpr int stream_ctas(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int stream_ctas(int nt) { return nt == 1 ? 4 : 2; }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a, int few_rows) {
@@ -160,7 +167,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
     const int per = (S.batch + T - 1) / T;
     auto seq_units = [&](const SeqInfo &q) {
         if ((int64_t)q.n * group > few_rows) return 0ll;         // attn_prompt_kernel's
-        const int tiles = (int)(((long long)q.n * group + R - 1) / R);
+        const int tiles = (q.n * group + R - 1) / R;
         const int units = q.len > 0 ? (q.len + kStreamUnit - 1) / kStreamUnit : 1;   // empty rows are written too
         return (long long)tiles * units * H;
     };
@@ -188,14 +195,21 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
         total += v;
     }
     before += scan - mine;
-    const long long G = min((long long)gridDim.x, total);
-    const long long c = blockIdx.x;
+    // range c holds `share` units, the first `more` ranges one more
+    const int G = (int)min((long long)gridDim.x, total), c = blockIdx.x;
     if (c >= G) {
         pdl_wait();
         return;
     }
-    long long u = total * c / G;
-    const long long u1 = total * (c + 1) / G;
+    const long long share = quotient(total, G);
+    const int more = (int)(total - share * G);
+    auto range_start = [&](int i) { return share * i + min(i, more); };
+    auto range_of = [&](long long unit) {
+        const long long head = (share + 1) * more;               // units of the longer ranges (share < 2^31: a range is below 2^37 tokens)
+        return unit < head ? (int)quotient(unit, (int)share + 1) : more + (int)quotient(unit - head, (int)share);
+    };
+    const long long u0 = range_start(c), u1 = range_start(c + 1);
+    long long u = u0;
     if (before <= u && u < before + mine) {
         long long x = before;
         int b = tid * per;
@@ -225,11 +239,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
             q = seq_info(S, b);
         }
         const int units = q.len > 0 ? (q.len + kStreamUnit - 1) / kStreamUnit : 1;
-        const int tiles = (int)(((long long)q.n * group + R - 1) / R);
+        const int rows = q.n * group, tiles = (rows + R - 1) / R;
         if (tiles == 0) break;                       // only if the lengths changed under the kernel
-        const long long tile_index = (u - seq_unit) / units;
-        const long long tile_unit = seq_unit + tile_index * units;
-        const int h = (int)(tile_index / tiles), rt = (int)(tile_index - (long long)h * tiles);
+        const int tile_index = (int)quotient(u - seq_unit, units);           // < tiles * H
+        const long long tile_unit = seq_unit + (long long)tile_index * units;
+        const int h = tile_index / tiles, rt = tile_index - h * tiles;
         const int unit0 = (int)(u - tile_unit);
         const int unit1 = (int)min((long long)units, u1 - tile_unit);
 
@@ -240,10 +254,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
         int most = 0, least = 0x7fffffff;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int64_t row = (int64_t)rt * R + 8 * nt + g;
-            const bool in = row < (int64_t)q.n * group;
-            const int64_t tok = row / group;
-            const int head = h * group + (int)(row - tok * group);
+            const int row = rt * R + 8 * nt + g;
+            const bool in = row < rows;
+            const int tok = row / group, head = h * group + row - tok * group;
             const uint16_t *src = a.q.p + (q.t0 + tok) * a.q.ts + (int64_t)head * a.q.hs;
             float y[CH][16];
             float top = 0.f;
@@ -276,8 +289,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
                     for (int k = 0; k < 2; ++k)
                         qf[nt][ch][i][k] = pack_half2(y[ch][4 * i + 2 * k] * up, y[ch][4 * i + 2 * k + 1] * up);
             const float down = a.scale * kLog2e * __int_as_float((127 - 14 + e) << 23);
-            int64_t seen = !in ? 0 : (a.causal ? (int64_t)q.len - q.n + tok + 1 : q.len);
-            const int v = (int)max((int64_t)0, min(seen, (int64_t)q.len));
+            const int v = !in ? 0 : a.causal ? min(max(q.len - q.n + tok + 1, 0), q.len) : q.len;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 f[nt][k] = __shfl_sync(0xffffffffu, down, (2 * t4 + k) * 4);
@@ -302,133 +314,139 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
         const int blk1 = min(unit1 * kStreamWarps, (most + 15) >> 4);
         const int32_t *pages = S.table + (int64_t)b * S.max_pages;
         const int bshift = S.page_shift - 4, bmask = (1 << bshift) - 1;
-        uint4 kr[2][2][CH];
-        uint32_t vr[2][4][VW];
-        float ks[2], vs[2];
+        uint4 kr[2][CH];
+        uint32_t vr[4][VW];
+        float ks = -1.f, vs = 0.f;
         auto page_of = [&](int blk) { return blk < blk1 ? __ldg(pages + (blk >> bshift)) : 0; };
-        auto load = [&](int blk, int page, int buf) {
-            if (blk >= blk1) return;
-            const bool ok = page >= 0 && page < S.pages;
-            if (!ok) {                               // no such page: its tokens are not seen
+        // where a block lies, in blocks of the cache; -1: no such page, its tokens are not seen
+        auto place = [&](int blk, int page) -> int64_t {
+            if (blk >= blk1) return -1;
+            if (page < 0 || page >= S.pages) {
                 if (lane == 0) report_invalid();
-                ks[buf] = -1.f;
-                return;
+                return -1;
             }
-            const int64_t sc = (((int64_t)page * H + h) << bshift) + (blk & bmask);
-            ks[buf] = __ldg(a.c.ks + sc);
-            vs[buf] = __ldg(a.c.vs + sc);
-            const int8_t *kp = a.c.k + sc * (16 * D), *vp = a.c.v + sc * (16 * D);
+            return (((int64_t)page * H + h) << bshift) + (blk & bmask);
+        };
+        auto load_k = [&](int64_t sc) {
+            ks = -1.f;
+            if (sc < 0) return;
+            ks = __ldg(a.c.ks + sc);
+            vs = __ldg(a.c.vs + sc);
+            const int8_t *kp = a.c.k + sc * (16 * D) + g * D + 16 * t4;
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int ch = 0; ch < CH; ++ch) kr[buf][r][ch] = ld_stream16(kp + (g + 8 * r) * D + 64 * ch + 16 * t4);
+                for (int ch = 0; ch < CH; ++ch) kr[r][ch] = ld_stream16(kp + 8 * r * D + 64 * ch);
+        };
+        auto load_v = [&](int64_t sc) {
+            if (sc < 0) return;
+            const int8_t *vp = a.c.v + sc * (16 * D) + 2 * t4 * D + g * (D / 8);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int8_t *p = vp + (2 * t4 + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
+                const int8_t *p = vp + ((r & 1) + 8 * (r >> 1)) * D;
                 if constexpr (VW == 4) {
                     const uint4 x = ld_stream16(p);
-                    vr[buf][r][0] = x.x, vr[buf][r][1] = x.y, vr[buf][r][2] = x.z, vr[buf][r][3] = x.w;
+                    vr[r][0] = x.x, vr[r][1] = x.y, vr[r][2] = x.z, vr[r][3] = x.w;
                 } else {
                     const uint2 x = ld_stream8(p);
-                    vr[buf][r][0] = x.x, vr[buf][r][1] = x.y;
+                    vr[r][0] = x.x, vr[r][1] = x.y;
                 }
-            }
-        };
-        auto work = [&](int blk, int buf) {
-            if (blk >= blk1 || ks[buf] < 0.f) return;
-            float s[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                const uint32_t w0[4] = {kr[buf][0][ch].x, kr[buf][0][ch].y, kr[buf][0][ch].z, kr[buf][0][ch].w};
-                const uint32_t w1[4] = {kr[buf][1][ch].x, kr[buf][1][ch].y, kr[buf][1][ch].z, kr[buf][1][ch].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t a0, a1, a2, a3;
-                    codes_to_half(w0[i], a0, a2);
-                    codes_to_half(w1[i], a1, a3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][ch][i][0], qf[nt][ch][i][1]);
-                }
-            }
-            const float ve = fmaxf(vs[buf], kLeastScale), lv = __log2f(ve), iv = __fdividef(1.f, ve);
-            const int at = blk * 16 + g;
-            const bool whole = blk * 16 + 16 <= least;
-            bool over = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    s[nt][k] = fmaf(s[nt][k], f[nt][k & 1] * ks[buf], lv);
-                    if (!whole && at + 8 * (k >> 1) >= vis[nt][k & 1]) s[nt][k] = -INFINITY;
-                    over |= s[nt][k] > m[nt][k & 1] + kLazy;
-                }
-            if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float x = fmaxf(s[nt][k], s[nt][k + 2]);
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        // by this row alone: what a row gets does not depend on its neighbours
-                        const float mn = x > m[nt][k] + kLazy ? x : m[nt][k];
-                        const float al = m[nt][k] == mn ? 1.f : ex2(m[nt][k] - mn);
-                        m[nt][k] = mn;
-                        l[nt][k] *= al;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) o[nt][i][k] *= al, o[nt][i][k + 2] *= al;
-                    }
-            }
-            uint32_t p0[NT], p1[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float mm = m[nt][k & 1] == -INFINITY ? 0.f : m[nt][k & 1];
-                    p[k] = ex2(s[nt][k] - mm + kPBias);
-                }
-                l[nt][0] = fmaf(p[0] + p[2], iv, l[nt][0]);
-                l[nt][1] = fmaf(p[1] + p[3], iv, l[nt][1]);
-                p0[nt] = movmatrix_trans(pack_half2(p[0], p[1]));
-                p1[nt] = movmatrix_trans(pack_half2(p[2], p[3]));
-            }
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-                // bytes of tokens (2 t4, 2 t4 + 1) and (2 t4 + 8, 2 t4 + 9) side by side, dims 4 w .. 4 w + 3
-                uint32_t x[2][4];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t lo = __byte_perm(vr[buf][2 * k][w], vr[buf][2 * k + 1][w], 0x5140);
-                    const uint32_t hi = __byte_perm(vr[buf][2 * k][w], vr[buf][2 * k + 1][w], 0x7362);
-                    codes_to_half(lo, x[k][0], x[k][1]);
-                    codes_to_half(hi, x[k][2], x[k][3]);
-                }
-#pragma unroll
-                for (int d = 0; d < 2; ++d)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16(o[nt][2 * w + d], x[0][2 * d], x[0][2 * d + 1], x[1][2 * d], x[1][2 * d + 1], p0[nt], p1[nt]);
             }
         };
         {
             int blk = unit0 * kStreamWarps + warp;
-            int page = page_of(blk), next = page_of(blk + kStreamWarps);
-            load(blk, page, 0);
-            while (blk < blk1) {
-                page = next;
-                next = page_of(blk + 2 * kStreamWarps);
-                load(blk + kStreamWarps, page, 1);
-                work(blk, 0);
-                blk += kStreamWarps;
-                page = next;
-                next = page_of(blk + 2 * kStreamWarps);
-                load(blk + kStreamWarps, page, 0);
-                work(blk, 1);
-                blk += kStreamWarps;
+            int64_t sc = place(blk, page_of(blk));
+            load_k(sc);
+            load_v(sc);
+            int page = page_of(blk + kStreamWarps);
+            for (; blk < blk1; blk += kStreamWarps) {
+                const int64_t next = place(blk + kStreamWarps, page);
+                page = page_of(blk + 2 * kStreamWarps);
+                const bool seen = ks >= 0.f;
+                float s[NT][4];
+                const float kscale = ks, ve = fmaxf(vs, kLeastScale);
+                if (seen) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+                    for (int ch = 0; ch < CH; ++ch) {
+                        const uint32_t w0[4] = {kr[0][ch].x, kr[0][ch].y, kr[0][ch].z, kr[0][ch].w};
+                        const uint32_t w1[4] = {kr[1][ch].x, kr[1][ch].y, kr[1][ch].z, kr[1][ch].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t a0, a1, a2, a3;
+                            codes_to_half(w0[i], a0, a2);
+                            codes_to_half(w1[i], a1, a3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][ch][i][0], qf[nt][ch][i][1]);
+                        }
+                    }
+                }
+                load_k(next);
+                if (seen) {
+                    const float lv = __log2f(ve), iv = __fdividef(1.f, ve);
+                    const int at = blk * 16 + g;
+                    const bool whole = blk * 16 + 16 <= least;
+                    bool over = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            s[nt][k] = fmaf(s[nt][k], f[nt][k & 1] * kscale, lv);
+                            if (!whole && at + 8 * (k >> 1) >= vis[nt][k & 1]) s[nt][k] = -INFINITY;
+                            over |= s[nt][k] > m[nt][k & 1] + kLazy;
+                        }
+                    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float x = fmaxf(s[nt][k], s[nt][k + 2]);
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                                // by this row alone: what a row gets does not depend on its neighbours
+                                const float mn = x > m[nt][k] + kLazy ? x : m[nt][k];
+                                const float al = m[nt][k] == mn ? 1.f : ex2(m[nt][k] - mn);
+                                m[nt][k] = mn;
+                                l[nt][k] *= al;
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) o[nt][i][k] *= al, o[nt][i][k + 2] *= al;
+                            }
+                    }
+                    uint32_t p0[NT], p1[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float p[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float mm = m[nt][k & 1] == -INFINITY ? 0.f : m[nt][k & 1];
+                            p[k] = ex2(s[nt][k] - mm + kPBias);
+                        }
+                        l[nt][0] = fmaf(p[0] + p[2], iv, l[nt][0]);
+                        l[nt][1] = fmaf(p[1] + p[3], iv, l[nt][1]);
+                        p0[nt] = movmatrix_trans(pack_half2(p[0], p[1]));
+                        p1[nt] = movmatrix_trans(pack_half2(p[2], p[3]));
+                    }
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        // bytes of tokens (2 t4, 2 t4 + 1) and (2 t4 + 8, 2 t4 + 9) side by side, dims 4 w .. 4 w + 3
+                        uint32_t x[2][4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t lo = __byte_perm(vr[2 * k][w], vr[2 * k + 1][w], 0x5140);
+                            const uint32_t hi = __byte_perm(vr[2 * k][w], vr[2 * k + 1][w], 0x7362);
+                            codes_to_half(lo, x[k][0], x[k][1]);
+                            codes_to_half(hi, x[k][2], x[k][3]);
+                        }
+#pragma unroll
+                        for (int d = 0; d < 2; ++d)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(o[nt][2 * w + d], x[0][2 * d], x[0][2 * d + 1], x[1][2 * d], x[1][2 * d + 1], p0[nt], p1[nt]);
+                    }
+                }
+                load_v(next);
             }
         }
 
@@ -452,13 +470,13 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
             }
         __syncthreads();
         const bool cut = unit0 > 0 || unit1 < units;
-        float *part = parts + ((long long)(2 * c) + (u == total * c / G ? 0 : 1)) * kPart;
+        float *part = parts + (2ll * c + (u == u0 ? 0 : 1)) * kPart;
         constexpr int PER = R * D / T;               // outputs of a thread, consecutive dims of one row
         const int r = tid * PER / D, d0 = tid * PER % D;
         auto write_out = [&](const float (&x)[PER], float M, float L) {
-            const int64_t row = (int64_t)rt * R + r;
-            if (row >= (int64_t)q.n * group) return;
-            const int64_t tok = row / group;
+            const int row = rt * R + r;
+            if (row >= rows) return;
+            const int tok = row / group;
             const int64_t at = (q.t0 + tok) * a.q_heads + h * group + (row - tok * group);
             const float inv = L == 0.f ? 0.f : 1.f / L;             // nothing seen: zeros
             uint32_t w[PER / 2];
@@ -488,45 +506,62 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
                 write_out(x, M, L);
             } else {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) __stcg(part + r * D + d0 + i, x[i]);
-                if (d0 == 0) {
-                    __stcg(part + R * D + 2 * r, M);
-                    __stcg(part + R * D + 2 * r + 1, L);
-                }
+                for (int i = 0; i < PER; i += 4)
+                    __stcg(reinterpret_cast<float4 *>(part + r * D + d0 + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+                if (d0 == 0) __stcg(reinterpret_cast<float2 *>(part + R * D) + r, make_float2(M, L));
             }
         }
         if (cut) {
             __threadfence();
             __syncthreads();
-            // ranges c0 .. c1 hold the tile; range c starts at total * c / G
-            auto range_of = [&](long long unit) {
-                long long x = unit * G / total;
-                while (x + 1 < G && total * (x + 1) / G <= unit) ++x;
-                while (x > 0 && total * x / G > unit) --x;
-                return x;
-            };
-            const long long c0 = range_of(tile_unit), c1 = range_of(tile_unit + units - 1);
+            const int c0 = range_of(tile_unit), c1 = range_of(tile_unit + units - 1);      // the ranges that hold the tile
             if (tid == 0) {
                 const int seen = atomicAdd(counters + c0, 1);
-                sm.last = seen == (int)(c1 - c0);
+                sm.last = seen == c1 - c0;
                 if (sm.last) counters[c0] = 0;
             }
             __syncthreads();
             if (sm.last) {
+                // the parts' maxima and sums first, all at once, then the sums in the order of the ranges, loads ahead
                 __threadfence();
+                float (*const pml)[2] = reinterpret_cast<float (*)[2]>(sm.o);
+                const int n_parts = c1 - c0 + 1, first_slot = range_start(c0) != tile_unit ? 1 : 0;
+                auto part_of = [&](int i) { return parts + (2ll * (c0 + i) + (i == 0 ? first_slot : 0)) * kPart; };
                 float M = -INFINITY, L = 0.f, x[PER];
 #pragma unroll
                 for (int i = 0; i < PER; ++i) x[i] = 0.f;
-                for (long long cc = c0; cc <= c1; ++cc) {
-                    const float *p = parts + (2 * cc + (cc == c0 && total * c0 / G != tile_unit ? 1 : 0)) * kPart;
-                    const float pm = __ldcg(p + R * D + 2 * r), pl = __ldcg(p + R * D + 2 * r + 1);
-                    if (pm == -INFINITY && pl == 0.f) continue;
-                    const float mn = fmaxf(M, pm);
-                    const float wa = M == -INFINITY ? 0.f : ex2(M - mn), wb = pm == -INFINITY ? pl : ex2(pm - mn);
-                    L = L * wa + pl * wb;
+                for (int p0 = 0; p0 < n_parts; p0 += kJoin) {
+                    const int np = min(kJoin, n_parts - p0);
+                    __syncthreads();
+                    for (int i = tid; i < np * R; i += T) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(part_of(p0 + i / R) + R * D) + i % R);
+                        pml[i][0] = v.x;
+                        pml[i][1] = v.y;
+                    }
+                    __syncthreads();
+                    float mn = M;
+                    for (int i = 0; i < np; ++i) mn = fmaxf(mn, pml[i * R + r][0]);
+                    const float wa = M == mn ? 1.f : ex2(M - mn);
+                    L *= wa;
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) x[i] = x[i] * wa + __ldcg(p + r * D + d0 + i) * wb;
+                    for (int i = 0; i < PER; ++i) x[i] *= wa;
                     M = mn;
+#pragma unroll 4
+                    for (int i = 0; i < np; ++i) {
+                        const float pm = pml[i * R + r][0], pl = pml[i * R + r][1];
+                        // nothing seen in a part: no weight, unless its sum says NaN
+                        const float w = pm == -INFINITY ? (pl == 0.f ? 0.f : pl) : ex2(pm - mn);
+                        const float4 *src = reinterpret_cast<const float4 *>(part_of(p0 + i) + r * D + d0);
+                        L = fmaf(pl, w, L);
+#pragma unroll
+                        for (int k = 0; k < PER / 4; ++k) {
+                            const float4 v = __ldcg(src + k);
+                            x[4 * k] = fmaf(v.x, w, x[4 * k]);
+                            x[4 * k + 1] = fmaf(v.y, w, x[4 * k + 1]);
+                            x[4 * k + 2] = fmaf(v.z, w, x[4 * k + 2]);
+                            x[4 * k + 3] = fmaf(v.w, w, x[4 * k + 3]);
+                        }
+                    }
                 }
                 write_out(x, M, L);
             }
