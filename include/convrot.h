@@ -511,7 +511,8 @@ convrot_status_t convrot_embed_lookup(const int32_t *tokens, int64_t t, const in
  * not overlap.  head_dim is 64 or 128.
  *
  * The paged cache: a VIEW of caller-owned device memory.
- *   k, v : int8 [pages, kv_heads, page_tokens, head_dim] codes
+ *   k, v : int8 [pages, kv_heads, page_tokens, head_dim] codes, 32-byte
+ *           aligned
  *   k_scale, v_scale : fp32 [pages, kv_heads, page_tokens / 16], one for
  *           every block of 16 tokens of a page and head: a code stands for
  *           code * scale
@@ -525,8 +526,10 @@ typedef struct {
     int32_t kv_heads, page_tokens, head_dim;
 } convrot_kv8_t;
 
-/* Fill a cache handle.  Checks: pointers non-NULL and 16-byte aligned, pages
-   1 .. 2^31 - 1, kv_heads 1 .. 4096, page_tokens and head_dim as above.  Host only. */
+/* Fill a cache handle.  Checks: pointers non-NULL and aligned, pages
+   1 .. 2^31 - 1, kv_heads 1 .. 4096, page_tokens and head_dim as above, at
+   most 2^31 - 1 blocks of 16 tokens and a head in all (2^41 bytes of codes and
+   more).  Host only. */
 convrot_status_t convrot_kv8_init(convrot_kv8_t *c, int8_t *k, int8_t *v, float *k_scale, float *v_scale,
                                   int64_t pages, int32_t kv_heads, int32_t page_tokens, int32_t head_dim);
 

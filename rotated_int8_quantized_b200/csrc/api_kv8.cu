@@ -16,9 +16,11 @@ convrot_status_t check_kv8(const convrot_kv8_t *c) {
     if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return CONVROT_ERR_INVALID_ARG;
     if (c->pages < 1 || c->kv_heads < 1 || c->page_tokens < 1) return CONVROT_ERR_INVALID_ARG;
     if (!head_dim_ok(c->head_dim) || !is_pow2(c->page_tokens) || c->page_tokens < convrot::kKvBlock ||
-        c->page_tokens > 1024 || c->kv_heads > kMaxHeads || c->pages > 0x7FFFFFFF)
+        c->page_tokens > 1024 || c->kv_heads > kMaxHeads || c->pages > 0x7FFFFFFF ||
+        c->pages * c->kv_heads * (c->page_tokens / convrot::kKvBlock) > 0x7FFFFFFF)     // blocks are counted in 32 bits
         return CONVROT_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+    // keys are read 32 bytes at a time
+    if (((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 31u) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
         return CONVROT_ERR_ALIGNMENT;
     return CONVROT_OK;
 }

@@ -84,6 +84,12 @@ __device__ __forceinline__ uint4 ld_stream16(const void *p) {
                  : "l"(p));
     return v;
 }
+// 32 bytes a lane, so that four lanes read a whole row of 128.
+__device__ __forceinline__ void ld_stream32(const void *p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
 __device__ __forceinline__ uint2 ld_stream8(const void *p) {
     uint2 v;
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
@@ -129,8 +135,8 @@ __device__ __forceinline__ SeqInfo seq_info(const KvSeqs &s, int b) {
 // w of every four blocks of 16 tokens, from global memory straight into the
 // operand layout of mma.m16n8k16 (16 tokens x 16 dims of K as the first
 // operand, 16 dims x 16 tokens of V; the sums run over dims, then tokens, in an
-// order of our choosing, so a lane simply takes 16 consecutive bytes of a row
-// and queries and outputs follow the same order).  The next block is in flight
+// order of our choosing, so a lane simply takes a quarter of a K row or an
+// eighth of a V row and queries and outputs follow the same order).  The next block is in flight
 // while one is worked on.
 //
 // Bound by memory, so the cache's blocks are dealt out evenly: all units (64
@@ -154,9 +160,8 @@ constexpr int stream_ctas(int nt) { return nt == 1 ? 4 : 2; }
 template <int D, int NT>
 __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a, int few_rows) {
     constexpr int R = 8 * NT, T = kStreamWarps * 32;
-    constexpr int CH = D / 64;                       // 16-byte chunks of a K row a lane holds
     constexpr int VW = D / 32;                       // words of a V row a lane holds
-    constexpr int MT = D / 16;
+    constexpr int MT = D / 16;                       // words of a K row a lane holds; 16-dim pieces of a row
     extern __shared__ __align__(16) uint8_t smem_raw[];
     StreamSmem<D, NT> &sm = *reinterpret_cast<StreamSmem<D, NT> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -247,34 +252,91 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
         const int unit0 = (int)(u - tile_unit);
         const int unit1 = (int)min((long long)units, u1 - tile_unit);
 
-        // queries: row 8 nt + g, dims 64 ch + 16 t4 .. + 15
-        uint32_t qf[NT][CH][4][2];
+        // what the tile's last and first row see
+        auto sees = [&](int tok) { return a.causal ? min(max(q.len - q.n + tok + 1, 0), q.len) : q.len; };
+        const int most = sees((min(rt * R + R, rows) - 1) / group), least = sees(rt * R / group);
+
+        // this warp's blocks: warp, warp + 4, .. of [4 unit0, 4 unit1), as far as a row sees
+        const int blk1 = min(unit1 * kStreamWarps, (most + 15) >> 4);
+        const int32_t *pages = S.table + (int64_t)b * S.max_pages;
+        const int bshift = S.page_shift - 4, bmask = (1 << bshift) - 1;
+        uint32_t kr[2][MT];
+        uint32_t vr[4][VW];
+        // Where this warp's blocks lie (in blocks of the cache; -1: no such page, its tokens are not seen) and their
+        // scales: a lane looks after one of the next 32.
+        int sc = -1;
+        float ks = 0.f, lv = 0.f, iv = 0.f;
+        auto look_up = [&](int first) {
+            const int blk = first + lane * kStreamWarps;
+            sc = -1;
+            if (blk >= blk1) return;
+            const int page = __ldg(pages + (blk >> bshift));
+            if (page < 0 || page >= S.pages) {
+                report_invalid();
+                return;
+            }
+            sc = ((page * H + h) << bshift) + (blk & bmask);         // < 2^31 (checked by the host)
+            const float ve = fmaxf(__ldg(a.c.vs + sc), kLeastScale);
+            ks = __ldg(a.c.ks + sc);
+            lv = __log2f(ve);
+            iv = __fdividef(1.f, ve);
+        };
+        const int8_t *const k0 = a.c.k + g * D + t4 * (D / 4), *const v0 = a.c.v + 2 * t4 * D + g * (D / 8);
+        auto load_k = [&](int sc) {
+            if (sc < 0) return;
+            const int8_t *kp = k0 + (int64_t)sc * (16 * D);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if constexpr (MT == 8) {
+                    ld_stream32(kp + 8 * r * D, kr[r]);
+                } else {
+                    const uint4 x = ld_stream16(kp + 8 * r * D);
+                    kr[r][0] = x.x, kr[r][1] = x.y, kr[r][2] = x.z, kr[r][3] = x.w;
+                }
+            }
+        };
+        auto load_v = [&](int sc) {
+            if (sc < 0) return;
+            const int8_t *vp = v0 + (int64_t)sc * (16 * D);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int8_t *p = vp + ((r & 1) + 8 * (r >> 1)) * D;
+                if constexpr (VW == 4) {
+                    const uint4 x = ld_stream16(p);
+                    vr[r][0] = x.x, vr[r][1] = x.y, vr[r][2] = x.z, vr[r][3] = x.w;
+                } else {
+                    const uint2 x = ld_stream8(p);
+                    vr[r][0] = x.x, vr[r][1] = x.y;
+                }
+            }
+        };
+        // the first block is on its way before the queries are looked at
+        int blk = unit0 * kStreamWarps + warp;
+        look_up(blk);
+        int now = __shfl_sync(0xffffffffu, sc, 0);
+        load_k(now);
+        load_v(now);
+
+        // queries: row 8 nt + g, dims (D / 4) t4 .. + D / 4 - 1
+        uint32_t qf[NT][MT][2];
         float f[NT][2];                              // rows 8 nt + 2 t4, + 1: log2(e) * softmax scale * row scale
         int vis[NT][2];                              // tokens they see
-        int most = 0, least = 0x7fffffff;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = rt * R + 8 * nt + g;
             const bool in = row < rows;
             const int tok = row / group, head = h * group + row - tok * group;
-            const uint16_t *src = a.q.p + (q.t0 + tok) * a.q.ts + (int64_t)head * a.q.hs;
-            float y[CH][16];
+            const uint16_t *src = a.q.p + (q.t0 + tok) * a.q.ts + (int64_t)head * a.q.hs + t4 * (D / 4);
+            uint32_t w[D / 8];
             float top = 0.f;
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                if (in) {
-                    x[0] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * ch + 16 * t4));
-                    x[1] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * ch + 16 * t4) + 1);
-                }
-                const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[ch][2 * i] = __uint_as_float(w[i] << 16);
-                    y[ch][2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                    top = fmaxf(top, fmaxf(fabsf(y[ch][2 * i]), fabsf(y[ch][2 * i + 1])));
-                }
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
             }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // 2^(14 - e), e the exponent of the row's largest element (held to what FP32 can scale by)
@@ -282,21 +344,17 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
             e = e > 127 ? 0 : (e < -100 ? -100 : e);
             const float up = __int_as_float((127 + 14 - e) << 23);
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        qf[nt][ch][i][k] = pack_half2(y[ch][4 * i + 2 * k] * up, y[ch][4 * i + 2 * k + 1] * up);
+                for (int k = 0; k < 2; ++k)
+                    qf[nt][i][k] = pack_half2(__uint_as_float(w[2 * i + k] << 16) * up, __uint_as_float(w[2 * i + k] & 0xFFFF0000u) * up);
             const float down = a.scale * kLog2e * __int_as_float((127 - 14 + e) << 23);
-            const int v = !in ? 0 : a.causal ? min(max(q.len - q.n + tok + 1, 0), q.len) : q.len;
+            const int v = in ? sees(tok) : most;                 // a row that is none only has to stay out of the way
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 f[nt][k] = __shfl_sync(0xffffffffu, down, (2 * t4 + k) * 4);
                 vis[nt][k] = __shfl_sync(0xffffffffu, v, (2 * t4 + k) * 4);
             }
-            most = max(most, __reduce_max_sync(0xffffffffu, v));
-            least = min(least, __reduce_min_sync(0xffffffffu, v));
         }
 
         float o[NT][MT][4], m[NT][2], l[NT][2];
@@ -310,90 +368,40 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
             l[nt][0] = l[nt][1] = 0.f;
         }
 
-        // this warp's blocks: warp, warp + 4, .. of [4 unit0, 4 unit1), as far as a row sees
-        const int blk1 = min(unit1 * kStreamWarps, (most + 15) >> 4);
-        const int32_t *pages = S.table + (int64_t)b * S.max_pages;
-        const int bshift = S.page_shift - 4, bmask = (1 << bshift) - 1;
-        uint4 kr[2][CH];
-        uint32_t vr[4][VW];
-        float ks = -1.f, vs = 0.f;
-        auto page_of = [&](int blk) { return blk < blk1 ? __ldg(pages + (blk >> bshift)) : 0; };
-        // where a block lies, in blocks of the cache; -1: no such page, its tokens are not seen
-        auto place = [&](int blk, int page) -> int64_t {
-            if (blk >= blk1) return -1;
-            if (page < 0 || page >= S.pages) {
-                if (lane == 0) report_invalid();
-                return -1;
-            }
-            return (((int64_t)page * H + h) << bshift) + (blk & bmask);
-        };
-        auto load_k = [&](int64_t sc) {
-            ks = -1.f;
-            if (sc < 0) return;
-            ks = __ldg(a.c.ks + sc);
-            vs = __ldg(a.c.vs + sc);
-            const int8_t *kp = a.c.k + sc * (16 * D) + g * D + 16 * t4;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch) kr[r][ch] = ld_stream16(kp + 8 * r * D + 64 * ch);
-        };
-        auto load_v = [&](int64_t sc) {
-            if (sc < 0) return;
-            const int8_t *vp = a.c.v + sc * (16 * D) + 2 * t4 * D + g * (D / 8);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int8_t *p = vp + ((r & 1) + 8 * (r >> 1)) * D;
-                if constexpr (VW == 4) {
-                    const uint4 x = ld_stream16(p);
-                    vr[r][0] = x.x, vr[r][1] = x.y, vr[r][2] = x.z, vr[r][3] = x.w;
-                } else {
-                    const uint2 x = ld_stream8(p);
-                    vr[r][0] = x.x, vr[r][1] = x.y;
-                }
-            }
-        };
         {
-            int blk = unit0 * kStreamWarps + warp;
-            int64_t sc = place(blk, page_of(blk));
-            load_k(sc);
-            load_v(sc);
-            int page = page_of(blk + kStreamWarps);
-            for (; blk < blk1; blk += kStreamWarps) {
-                const int64_t next = place(blk + kStreamWarps, page);
-                page = page_of(blk + 2 * kStreamWarps);
-                const bool seen = ks >= 0.f;
+            for (int at = 0; blk < blk1; blk += kStreamWarps) {
+                const bool seen = now >= 0;
+                const float kscale = __shfl_sync(0xffffffffu, ks, at), vlog = __shfl_sync(0xffffffffu, lv, at),
+                            vinv = __shfl_sync(0xffffffffu, iv, at);
+                if (++at == 32) {
+                    at = 0;
+                    look_up(blk + kStreamWarps);
+                }
+                const int next = __shfl_sync(0xffffffffu, sc, at);
                 float s[NT][4];
-                const float kscale = ks, ve = fmaxf(vs, kLeastScale);
                 if (seen) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-                    for (int ch = 0; ch < CH; ++ch) {
-                        const uint32_t w0[4] = {kr[0][ch].x, kr[0][ch].y, kr[0][ch].z, kr[0][ch].w};
-                        const uint32_t w1[4] = {kr[1][ch].x, kr[1][ch].y, kr[1][ch].z, kr[1][ch].w};
+                    for (int i = 0; i < MT; ++i) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_to_half(kr[0][i], a0, a2);
+                        codes_to_half(kr[1][i], a1, a3);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t a0, a1, a2, a3;
-                            codes_to_half(w0[i], a0, a2);
-                            codes_to_half(w1[i], a1, a3);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][ch][i][0], qf[nt][ch][i][1]);
-                        }
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][i][0], qf[nt][i][1]);
                     }
                 }
                 load_k(next);
                 if (seen) {
-                    const float lv = __log2f(ve), iv = __fdividef(1.f, ve);
-                    const int at = blk * 16 + g;
+                    const int tok = blk * 16 + g;
                     const bool whole = blk * 16 + 16 <= least;
                     bool over = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            s[nt][k] = fmaf(s[nt][k], f[nt][k & 1] * kscale, lv);
-                            if (!whole && at + 8 * (k >> 1) >= vis[nt][k & 1]) s[nt][k] = -INFINITY;
+                            s[nt][k] = fmaf(s[nt][k], f[nt][k & 1] * kscale, vlog);
+                            if (!whole && tok + 8 * (k >> 1) >= vis[nt][k & 1]) s[nt][k] = -INFINITY;
                             over |= s[nt][k] > m[nt][k & 1] + kLazy;
                         }
                     if (__any_sync(0xffffffffu, over)) {
@@ -423,8 +431,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
                             const float mm = m[nt][k & 1] == -INFINITY ? 0.f : m[nt][k & 1];
                             p[k] = ex2(s[nt][k] - mm + kPBias);
                         }
-                        l[nt][0] = fmaf(p[0] + p[2], iv, l[nt][0]);
-                        l[nt][1] = fmaf(p[1] + p[3], iv, l[nt][1]);
+                        l[nt][0] = fmaf(p[0] + p[2], vinv, l[nt][0]);
+                        l[nt][1] = fmaf(p[1] + p[3], vinv, l[nt][1]);
                         p0[nt] = movmatrix_trans(pack_half2(p[0], p[1]));
                         p1[nt] = movmatrix_trans(pack_half2(p[2], p[3]));
                     }
@@ -447,6 +455,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
                     }
                 }
                 load_v(next);
+                now = next;
             }
         }
 

@@ -43,7 +43,8 @@ def _rope(**kw):
     ({}, OK), (dict(k=0), INVALID), (dict(v_scale=0), INVALID), (dict(pages=0), INVALID), (dict(kv_heads=0), INVALID),
     (dict(kv_heads=4097), SHAPE), (dict(page_tokens=8), SHAPE), (dict(page_tokens=48), SHAPE), (dict(page_tokens=2048), SHAPE),
     (dict(page_tokens=16), OK), (dict(page_tokens=1024), OK), (dict(head_dim=96), SHAPE), (dict(head_dim=64), OK),
-    (dict(pages=2 ** 31), SHAPE), (dict(k=0x10008), ALIGN), (dict(k_scale=0x30004), ALIGN)])
+    (dict(pages=2 ** 31), SHAPE), (dict(k=0x10008), ALIGN), (dict(k=0x10010), ALIGN),
+    (dict(v=0x20010), ALIGN), (dict(k_scale=0x30004), ALIGN)])
 def test_cache_handle(lib, kw, want):
     c, out = _cache(**kw), cr.convrot_kv8_t()
     assert lib.convrot_kv8_init(ctypes.byref(out), c.k, c.v, c.k_scale, c.v_scale, c.pages, c.kv_heads, c.page_tokens,
