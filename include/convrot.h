@@ -539,7 +539,7 @@ convrot_status_t convrot_kv8_init(convrot_kv8_t *c, int8_t *k, int8_t *v, float 
  *   cos_sin  : fp32 [positions, rot_dim / 2, 2] (device)
  *   rot_dim  : a multiple of 8, 8 .. head_dim; the dims behind it stay
  *   adjacent : 0: pair i is dims (i, i + rot_dim / 2);  1: dims (2 i, 2 i + 1)
- *   axis     : uint8 [rot_dim / 2] (device): the row of `positions` that pair
+ *   axis     : uint8 [rot_dim / 2] (device, 4-byte aligned): the row of `positions` that pair
  *              i goes by (several position axes: time, height, width), or
  *              NULL: row 0 for all
  *   axes     : rows of the positions, 1 .. 8

@@ -49,7 +49,7 @@ convrot_status_t check_rope(const convrot_rope_t *r, const int32_t *positions, i
     if (needs_positions && !positions) return CONVROT_ERR_INVALID_ARG;
     if (!positions && (r->axis || r->axes != 1)) return CONVROT_ERR_INVALID_ARG;
     if (r->rot_dim < 8 || r->rot_dim > dim || r->rot_dim % 8 != 0) return CONVROT_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(r->cos_sin) || (positions && (reinterpret_cast<uintptr_t>(positions) & 3u)))
+    if (!aligned16(r->cos_sin) || ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(r->axis)) & 3u))
         return CONVROT_ERR_ALIGNMENT;
     out->cs = r->cos_sin;
     out->rows = r->positions;

@@ -129,9 +129,10 @@ __device__ __forceinline__ bool load_rotation(const RopeArgs &r, const LaneGeo &
         return true;
     }
     bool ok = true;
+    const uchar4 axes = __ldg(reinterpret_cast<const uchar4 *>(r.axis) + lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int ax = __ldg(r.axis + 4 * lane + i);
+        const int ax = i == 0 ? axes.x : i == 1 ? axes.y : i == 2 ? axes.z : axes.w;
         const int64_t p = ax < r.axes ? (int64_t)__ldg(r.pos + ax * tokens + t) : -1;
         if (p < 0 || p >= r.rows) {
             ok = false;
@@ -201,31 +202,41 @@ __device__ __forceinline__ void load_weight(const uint16_t *w, const LaneGeo &g,
     unpack_bf16x4(__ldg(reinterpret_cast<const uint2 *>(w + g.b)), out + 4);
 }
 
-// Heads [h0, h1) of token row t: load, norm, rotate, round, store.  Rows may
-// be rotated in place, so plain loads.
-template <int L>
+// Heads [h0, h1) of token row t: load, norm, rotate, round, store, four rows
+// in flight and the next four behind them.  `rotation` fetches the
+// coefficients (and says whether to write zeros) once the first rows are on
+// their way.  Rows may be rotated in place, so plain loads.
+template <int L, typename Rotation>
 __device__ __forceinline__ void head_rows(const HeadRows &in, const HeadRowsOut &out, int64_t t, int h0, int h1,
-                                          const uint16_t *weight, float eps, const LaneGeo &g, bool adjacent, bool zero,
-                                          const float (&c)[4], const float (&s)[4]) {
-    constexpr int U = 4;                  // rows in flight
-    float w[8];
-    load_weight(weight, g, w);
+                                          const uint16_t *weight, float eps, const LaneGeo &g, bool adjacent,
+                                          Rotation rotation) {
+    constexpr int U = 2;
     const uint16_t *src = in.p + t * in.ts;
     uint16_t *dst = out.p + t * out.ts;
-    for (int h = h0; h < h1; h += U) {
-        uint2 x[U][2];
+    uint2 x[U][2];
+    auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (h + u < h1) {
                 x[u][0] = *reinterpret_cast<const uint2 *>(src + (h + u) * in.hs + g.a);
                 x[u][1] = *reinterpret_cast<const uint2 *>(src + (h + u) * in.hs + g.b);
             }
+    };
+    load(h0);
+    float w[8], c[4], s[4];
+    load_weight(weight, g, w);
+    const bool zero = !rotation(c, s);
+    for (int h = h0; h < h1; h += U) {
+        uint2 now[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u][0] = x[u][0], now[u][1] = x[u][1];
+        load(h + U);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (h + u < h1) {
                 float y[8];
-                unpack_bf16x4(x[u][0], y);
-                unpack_bf16x4(x[u][1], y + 4);
+                unpack_bf16x4(now[u][0], y);
+                unpack_bf16x4(now[u][1], y + 4);
                 norm_rotate<L>(y, w, weight != nullptr, eps, g, adjacent, c, s);
                 uint2 lo = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
                 uint2 hi = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
@@ -243,7 +254,7 @@ __device__ __forceinline__ bool all_lanes(bool ok) {
 }
 
 template <int L>
-__global__ void __launch_bounds__(kHeadThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per, int cq,
+__global__ void __launch_bounds__(kHeadThreads, 4) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per, int cq,
                                                                int chunks) {
     const int lane = threadIdx.x & (L - 1);
     const int64_t task = (int64_t)blockIdx.x * (kHeadThreads / L) + threadIdx.x / L;
@@ -251,31 +262,41 @@ __global__ void __launch_bounds__(kHeadThreads) norm_rope_kernel(const __grid_co
     if (t >= a.tokens) return;
     const int ch = (int)(task - t * chunks);
     const LaneGeo g = lane_geo(lane, a.rope);
-    float c[4], s[4];
-    const bool ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.tokens, -1, c, s));
-    if (!ok && lane == 0) report_invalid();
+    auto rotation = [&](float (&c)[4], float (&s)[4]) {
+        const bool ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.tokens, -1, c, s));
+        if (!ok && lane == 0) report_invalid();
+        return ok;
+    };
     if (ch < cq) {
         const int h0 = ch * per;
-        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent, !ok, c, s);
+        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent, rotation);
     } else {
         const int h0 = (ch - cq) * per;
-        head_rows<L>(a.k, a.k_out, t, h0, min(h0 + per, a.kv_heads), a.kw, a.eps, g, a.rope.adjacent, !ok, c, s);
+        head_rows<L>(a.k, a.k_out, t, h0, min(h0 + per, a.kv_heads), a.kw, a.eps, g, a.rope.adjacent, rotation);
     }
 }
 
 // Heads a lane group takes one after another: one while there are few rows
 // (latency), up to eight once the GPU is full (the table entries and weights
 // are then loaded once for eight heads).
+constexpr int kMostPer = 8;
 static int heads_per_group(int64_t tokens, int heads, int lanes, int sms) {
     const int64_t groups = (int64_t)sms * 2048 / lanes;
     int per = 1;
-    while (per < 8 && tokens * heads > groups * per * 2) per *= 2;
+    while (per < kMostPer && tokens * heads > groups * per * 2) per *= 2;
     return per;
+}
+
+// The same for each of `heads`' chunks.
+static int even(int heads, int per) {
+    if (heads == 0) return 1;
+    const int chunks = (heads + per - 1) / per;
+    return (heads + chunks - 1) / chunks;
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int sms, cudaStream_t stream) {
     const int L = a.dim / 8;
-    const int per = heads_per_group(a.tokens, a.q_heads + a.kv_heads, L, sms);
+    const int per = even(a.q_heads, heads_per_group(a.tokens, a.q_heads + a.kv_heads, L, sms));
     const int cq = (a.q_heads + per - 1) / per, chunks = cq + (a.kv_heads + per - 1) / per;
     const int64_t blocks = (a.tokens * chunks + kHeadThreads / L - 1) / (kHeadThreads / L);
     if (L == 16)
@@ -329,12 +350,11 @@ __device__ __forceinline__ float grow_scale(float most, bool held, float old, fl
 // CTA = 16 rows x L lanes: one block of 16 tokens of one head, keys and
 // values together (blockIdx.x < kv_ctas), or chunks of the queries' heads.
 template <int L>
-__global__ void __launch_bounds__(16 * L) kv8_append_kernel(const __grid_constant__ AppendArgs a, int64_t kv_ctas, int per,
+__global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid_constant__ AppendArgs a, int64_t kv_ctas, int per,
                                                           int chunks) {
     const int lane = threadIdx.x & (L - 1), row = threadIdx.x / L;
     const LaneGeo g = lane_geo(lane, a.rope);
     const int64_t cap = (int64_t)a.s.max_pages << a.s.page_shift;
-    float c[4], s[4];
     if ((int64_t)blockIdx.x >= kv_ctas) {
         // ---------------------------------------------------- queries
         const int64_t task = ((int64_t)blockIdx.x - kv_ctas) * 16 + row;
@@ -342,12 +362,16 @@ __global__ void __launch_bounds__(16 * L) kv8_append_kernel(const __grid_constan
         if (t >= a.s.tokens) return;
         const TokenPlace p = place_token<L>(a.s, t);
         if (p.b < 0) return;
-        const bool pad = p.pos < 0;
-        bool ok = true;
-        if (!pad) ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.s.tokens, p.pos, c, s)) && p.pos < cap;
-        if (!ok && lane == 0) report_invalid();
         const int h0 = (int)(task - t * chunks) * per;
-        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent, pad || !ok, c, s);
+        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent,
+                     [&](float (&c)[4], float (&s)[4]) {
+#pragma unroll
+                         for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
+                         if (p.pos < 0) return false;                       // padding: zeros
+                         const bool ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.s.tokens, p.pos, c, s)) && p.pos < cap;
+                         if (!ok && lane == 0) report_invalid();
+                         return ok;
+                     });
         return;
     }
     // -------------------------------------------------------- keys, values
@@ -386,30 +410,34 @@ __global__ void __launch_bounds__(16 * L) kv8_append_kernel(const __grid_constan
         if (blk * kKvBlock >= cap) return;
     }
     const int64_t page = __ldg(a.s.table + (int64_t)b * a.s.max_pages + (blk * kKvBlock >> a.s.page_shift));
-    if (page < 0 || page >= a.s.pages) {
-        if (threadIdx.x == 0) report_invalid();
-        return;
-    }
     const int64_t pos = blk * kKvBlock + row;
     const bool fresh = pos >= first && pos < len;
     const bool held = blk * kKvBlock < first;               // the block has older tokens
     const int64_t t = t0 + n - (len - pos);
-    float k[8], v[8], mk = 0.f, mv = 0.f;
-    const int blocks = 1 << (a.s.page_shift - 4), in_page = (int)(blk & (blocks - 1));
-    const int64_t sc = (page * H + h) * blocks + in_page;
-    const float old_k = held ? a.c.ks[sc] : 0.f, old_v = held ? a.c.vs[sc] : 0.f;
+    // the row's values and coefficients are on their way before the page is known
+    float k[8], v[8], w[8], c[4], s[4], mk = 0.f, mv = 0.f;
+    uint2 x[4];
     bool ok = true;
     if (fresh) {
         const uint16_t *kp = a.k.p + t * a.k.ts + h * a.k.hs, *vp = a.v.p + t * a.v.ts + h * a.v.hs;
-        const uint2 k0 = __ldg(reinterpret_cast<const uint2 *>(kp + g.a)), k1 = __ldg(reinterpret_cast<const uint2 *>(kp + g.b));
-        const uint2 v0 = __ldg(reinterpret_cast<const uint2 *>(vp + g.a)), v1 = __ldg(reinterpret_cast<const uint2 *>(vp + g.b));
-        float w[8];
+        x[0] = __ldg(reinterpret_cast<const uint2 *>(kp + g.a)), x[1] = __ldg(reinterpret_cast<const uint2 *>(kp + g.b));
+        x[2] = __ldg(reinterpret_cast<const uint2 *>(vp + g.a)), x[3] = __ldg(reinterpret_cast<const uint2 *>(vp + g.b));
         load_weight(a.kw, g, w);
-        ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.s.tokens, pos, c, s));
-        unpack_bf16x4(k0, k);
-        unpack_bf16x4(k1, k + 4);
-        unpack_bf16x4(v0, v);
-        unpack_bf16x4(v1, v + 4);
+        ok = load_rotation(a.rope, g, lane, t, a.s.tokens, pos, c, s);
+    }
+    if (page < 0 || page >= a.s.pages) {
+        if (threadIdx.x == 0) report_invalid();
+        return;
+    }
+    const int blocks = 1 << (a.s.page_shift - 4), in_page = (int)(blk & (blocks - 1));
+    const int64_t sc = (page * H + h) * blocks + in_page;
+    const float old_k = held ? a.c.ks[sc] : 0.f, old_v = held ? a.c.vs[sc] : 0.f;
+    if (fresh) {
+        ok = all_lanes<L>(ok);
+        unpack_bf16x4(x[0], k);
+        unpack_bf16x4(x[1], k + 4);
+        unpack_bf16x4(x[2], v);
+        unpack_bf16x4(x[3], v + 4);
         norm_rotate<L>(k, w, a.kw != nullptr, a.eps, g, a.rope.adjacent, c, s);
         if (!ok) {
             if (lane == 0) report_invalid();
@@ -457,7 +485,7 @@ cudaError_t launch_kv8_append(const AppendArgs &a, int sms, cudaStream_t stream)
     const int L = a.c.dim / 8;
     const int64_t slots = a.s.cu ? a.s.tokens / kKvBlock + 2 * (int64_t)a.s.batch : a.s.batch;
     const int64_t kv_ctas = slots * a.c.heads;
-    const int per = a.q_heads ? heads_per_group(a.s.tokens, a.q_heads, L, sms) : 1;
+    const int per = even(a.q_heads, heads_per_group(a.s.tokens, a.q_heads, L, sms));
     const int chunks = (a.q_heads + per - 1) / per;
     const int64_t blocks = kv_ctas + (a.s.tokens * chunks + 15) / 16;
     if (L == 16)
@@ -500,19 +528,29 @@ __global__ void __launch_bounds__(kHeadThreads) kv8_read_kernel(const __grid_con
     }
     const int in_page = (int)(p.pos & ((1 << a.s.page_shift) - 1));
     const int h0 = (int)(task - t * chunks) * per, h1 = min(h0 + per, H);
-    for (int h = h0; h < h1; ++h) {
-        uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-        if (page >= 0) {
-            const int64_t r = ((page * H + h) << a.s.page_shift) + in_page;
-            const float ks = __ldg(a.c.ks + (r >> 4)), vs = __ldg(a.c.vs + (r >> 4));
-            const uint2 kc = __ldg(reinterpret_cast<const uint2 *>(a.c.k + r * D) + lane);
-            const uint2 vc = __ldg(reinterpret_cast<const uint2 *>(a.c.v + r * D) + lane);
-            k = dequant8(kc, ks);
-            v = dequant8(vc, vs);
+    constexpr int U = 4;                  // heads in flight
+    for (int h = h0; h < h1; h += U) {
+        uint2 kc[U], vc[U];
+        float ks[U], vs[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            kc[u] = vc[u] = make_uint2(0u, 0u);
+            ks[u] = vs[u] = 0.f;
+            if (page >= 0 && h + u < h1) {
+                const int64_t r = ((page * H + h + u) << a.s.page_shift) + in_page;
+                ks[u] = __ldg(a.c.ks + (r >> 4));
+                vs[u] = __ldg(a.c.vs + (r >> 4));
+                kc[u] = __ldg(reinterpret_cast<const uint2 *>(a.c.k + r * D) + lane);
+                vc[u] = __ldg(reinterpret_cast<const uint2 *>(a.c.v + r * D) + lane);
+            }
         }
-        const int64_t o = (t * H + h) * L + lane;
-        if (a.k_out) reinterpret_cast<uint4 *>(a.k_out)[o] = k;
-        if (a.v_out) reinterpret_cast<uint4 *>(a.v_out)[o] = v;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (h + u < h1) {
+                const int64_t o = (t * H + h + u) * L + lane;
+                if (a.k_out) reinterpret_cast<uint4 *>(a.k_out)[o] = dequant8(kc[u], ks[u]);
+                if (a.v_out) reinterpret_cast<uint4 *>(a.v_out)[o] = dequant8(vc[u], vs[u]);
+            }
     }
 }
 

@@ -78,7 +78,7 @@ def _norm_job(rope=None, **kw):
     (dict(q_weight=0x8), None, ALIGN), (dict(eps=-1.0), None, INVALID), (dict(eps=float("nan")), None, INVALID),
     ({}, dict(cos_sin=0), INVALID), ({}, dict(rot_dim=12), SHAPE), ({}, dict(rot_dim=136), SHAPE), ({}, dict(rot_dim=0), SHAPE),
     ({}, dict(axes=9), INVALID), ({}, dict(axes=0), INVALID), ({}, dict(positions=0), INVALID), ({}, dict(cos_sin=0x80008), ALIGN),
-    (dict(positions=0), {}, INVALID), (dict(positions=0x90002), {}, ALIGN)])
+    ({}, dict(axis=0x90002), ALIGN), (dict(positions=0), {}, INVALID), (dict(positions=0x90002), {}, ALIGN)])
 def test_norm_rope_refusals(lib, kw, rope, want):
     job = _norm_job(None if rope is None else _rope(**rope), **kw)
     assert lib.convrot_qk_norm_rope(ctypes.byref(job), None) == want
