@@ -98,6 +98,14 @@ __device__ __forceinline__ uint2 ld_stream8(const void *p) {
 
 // Rows, cached tokens and first row of sequence b, held to the step's bounds
 // whatever the device arrays say.
+// An atomic add that orders this thread's (and, behind a barrier, its CTA's)
+// accesses on both sides of it.
+__device__ __forceinline__ int add_acq_rel(int *p, int v) {
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 // a / b for a >= 0 and b > 0, in 32 bits where they do (a 64-bit quotient is a
 // quarter of a microsecond, and several stand between a small call and its end).
 __device__ __forceinline__ long long quotient(long long a, int b) {
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
         // Where this warp's blocks lie (in blocks of the cache; -1: no such page, its tokens are not seen) and their
         // scales: a lane looks after one of the next 32.
         int sc = -1;
-        float ks = 0.f, lv = 0.f, iv = 0.f;
+        float ks = 0.f, vs = 0.f, lv = 0.f, iv = 0.f;
         auto look_up = [&](int first) {
             const int blk = first + lane * kStreamWarps;
             sc = -1;
@@ -276,8 +284,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
                 return;
             }
             sc = ((page * H + h) << bshift) + (blk & bmask);         // < 2^31 (checked by the host)
-            const float ve = fmaxf(__ldg(a.c.vs + sc), kLeastScale);
             ks = __ldg(a.c.ks + sc);
+            vs = __ldg(a.c.vs + sc);
+        };
+        auto scales = [&] {                          // apart, so that nothing waits for them before the codes are asked for
+            const float ve = fmaxf(vs, kLeastScale);
             lv = __log2f(ve);
             iv = __fdividef(1.f, ve);
         };
@@ -316,6 +327,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
         int now = __shfl_sync(0xffffffffu, sc, 0);
         load_k(now);
         load_v(now);
+        scales();
 
         // queries: row 8 nt + g, dims (D / 4) t4 .. + D / 4 - 1
         uint32_t qf[NT][MT][2];
@@ -376,6 +388,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
                 if (++at == 32) {
                     at = 0;
                     look_up(blk + kStreamWarps);
+                    scales();
                 }
                 const int next = __shfl_sync(0xffffffffu, sc, at);
                 float s[NT][4];
@@ -521,18 +534,16 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
             }
         }
         if (cut) {
-            __threadfence();
             __syncthreads();
             const int c0 = range_of(tile_unit), c1 = range_of(tile_unit + units - 1);      // the ranges that hold the tile
             if (tid == 0) {
-                const int seen = atomicAdd(counters + c0, 1);
+                const int seen = add_acq_rel(counters + c0, 1);         // releases the whole CTA's part (barrier above)
                 sm.last = seen == c1 - c0;
                 if (sm.last) counters[c0] = 0;
             }
             __syncthreads();
             if (sm.last) {
                 // the parts' maxima and sums first, all at once, then the sums in the order of the ranges, loads ahead
-                __threadfence();
                 float (*const pml)[2] = reinterpret_cast<float (*)[2]>(sm.o);
                 const int n_parts = c1 - c0 + 1, first_slot = range_start(c0) != tile_unit ? 1 : 0;
                 auto part_of = [&](int i) { return parts + (2ll * (c0 + i) + (i == 0 ? first_slot : 0)) * kPart; };
