@@ -115,7 +115,7 @@ convrot_status_t check_attn(const convrot_attn_kv8_t *job, convrot::AttnArgs *a)
 }
 
 size_t attn_bytes(const convrot::AttnArgs &a, int sms) {
-    return round256((size_t)convrot::attn_kv8_workspace_bytes(a.s.tokens, a.s.batch, a.q_heads, a.c.heads, a.c.dim, sms));
+    return round256((size_t)convrot::attn_kv8_workspace_bytes(a, sms));
 }
 
 }  // namespace

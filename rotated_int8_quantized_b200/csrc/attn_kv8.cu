@@ -616,6 +616,31 @@ constexpr int kPromptWarps = 16;
 constexpr int kPromptRows = 256;                     // two tiles
 constexpr int kKvTile = 128;
 constexpr int kInfoRing = 4;
+// Where there are too few tile pairs for the GPU, several CTAs share a pair's
+// pass over the cache, each a range of its steps (two at least), and leave FP32
+// sums and maxima in the workspace for attn_join_kernel: 192 rows on 8192
+// tokens at 8 key heads are 8 pairs, 64 steps each, for 148 SMs.
+constexpr int kMostSplit = 16;
+
+// Ranges that a pass of `steps` is cut into, of `split` at the most.
+__host__ __device__ __forceinline__ int prompt_ranges(int steps, int split) {
+    const int n = steps / 2 < split ? steps / 2 : split;
+    return n < 1 ? 1 : n;
+}
+
+// A tile pair: sequence, slot within it, rows, and the steps of its pass.
+struct PromptTile {
+    int b, steps;
+    SeqInfo q;
+    int64_t rows, row0;
+};
+
+// Where a range's part lies: [kPromptRows][D] sums, then [kPromptRows] pairs
+// of maximum and weights' sum.
+template <int D>
+__device__ __forceinline__ float *prompt_part(float *parts, int64_t pair, int split, int range) {
+    return parts + (pair * split + range) * (int64_t)(kPromptRows * (D + 2));
+}
 
 template <int D>
 struct PromptSmem {
@@ -689,8 +714,36 @@ __device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Sequence b owns the slots from floor(cu[b] group / 256) + b on, at least as
+// many as it has pairs of tiles.  Called by a whole warp; -1: none.
+__device__ __forceinline__ int find_slot(const AttnArgs &a, int64_t slot, int &within) {
+    const int group = a.q_heads / a.c.heads;
+    auto first_slot = [&](int i) {
+        const int64_t t0 = a.s.cu ? (int64_t)__ldg(a.s.cu + i) : i;
+        return t0 * group / kPromptRows + i;
+    };
+    const int b = search_lanes<32>(a.s.batch, slot, first_slot);
+    within = b < 0 ? 0 : (int)(slot - first_slot(b));
+    return b;
+}
+
+__device__ __forceinline__ bool prompt_tile(const AttnArgs &a, int b, int slot, int few_rows, PromptTile &t) {
+    const int group = a.q_heads / a.c.heads;
+    t.b = b;
+    t.q = seq_info(a.s, b);
+    t.rows = (int64_t)t.q.n * group;
+    t.row0 = (int64_t)slot * kPromptRows;
+    if (t.rows <= few_rows || t.row0 >= t.rows) return false;
+    // what the last row sees is what any row sees
+    const int64_t tok = (min(t.rows, t.row0 + kPromptRows) - 1) / group;
+    const int64_t most = a.causal ? max((int64_t)0, min((int64_t)t.q.len, (int64_t)t.q.len - t.q.n + tok + 1)) : t.q.len;
+    t.steps = (int)((most + kKvTile - 1) / kKvTile);
+    return true;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const __grid_constant__ AttnArgs a, int few_rows) {
+__global__ void __launch_bounds__(kPromptWarps * 32, 1)
+    attn_prompt_kernel(const __grid_constant__ AttnArgs a, int few_rows, int split, float *parts) {
     constexpr int DB = D / 64;                       // 128-byte row blocks of an operand
     constexpr uint32_t kBlockBytes = 128 * 128;
     extern __shared__ uint8_t smem_raw[];
@@ -699,32 +752,29 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
     const int H = a.c.heads, group = a.q_heads / H;
     const KvSeqs &S = a.s;
 
-    // The tile pair of this CTA; sequence b owns the slots from floor(cu[b] group / 256) + b on.  Last ones first: under a
-    // causal mask they are the longest.
+    // The tile pair of this CTA.  Last ones first: under a causal mask they are the longest.
     pdl_launch_dependents();                         // attn_stream_kernel waits for this one at its end only
-    const int64_t slots = gridDim.x / H;
-    const int64_t slot = slots - 1 - blockIdx.x / H;
-    const int h = blockIdx.x % H;
-    auto first_slot = [&](int i) {
-        const int64_t t0 = S.cu ? (int64_t)__ldg(S.cu + i) : i;
-        return t0 * group / kPromptRows + i;
-    };
+    const int64_t pairs = gridDim.x / split, pair = pairs - 1 - blockIdx.x / split;
+    const int h = pair % H;
     if (warp == 0) {
-        const int b = search_lanes<32>(S.batch, slot, first_slot);
-        if (lane == 0) sm.seq = b, sm.slot = b < 0 ? 0 : (int)(slot - first_slot(b));
+        int slot;
+        const int b = find_slot(a, pair / H, slot);
+        if (lane == 0) sm.seq = b, sm.slot = slot;
     }
     __syncthreads();
     const int b = sm.seq;
     if (b < 0) return;
-    const SeqInfo q = seq_info(S, b);
+    PromptTile tile;
+    if (!prompt_tile(a, b, sm.slot, few_rows, tile)) return;
+    const SeqInfo &q = tile.q;
     if (q.bad && tid == 0) report_invalid();
-    const int64_t rows = (int64_t)q.n * group, row0 = (int64_t)sm.slot * kPromptRows;
-    if (rows <= few_rows || row0 >= rows) return;
+    const int64_t rows = tile.rows, row0 = tile.row0;
     const int tiles = rows - row0 > 128 ? 2 : 1;
-    // what the last row sees is what any row sees
-    const int64_t last_tok = (min(rows, row0 + kPromptRows) - 1) / group;
-    const int64_t most = a.causal ? max((int64_t)0, min((int64_t)q.len, (int64_t)q.len - q.n + last_tok + 1)) : q.len;
-    const int steps = (int)((most + kKvTile - 1) / kKvTile);
+    // this CTA's range of the pass
+    const int ranges = prompt_ranges(tile.steps, split), range = blockIdx.x % split;
+    if (range >= ranges) return;
+    const int step0 = (int)((int64_t)tile.steps * range / ranges);
+    const int steps = (int)((int64_t)tile.steps * (range + 1) / ranges) - step0;
 
     const uint32_t q_full = smem_addr(&sm.q_full), k_full = smem_addr(sm.k_full), k_empty = smem_addr(sm.k_empty),
                    v_full = smem_addr(sm.v_full), v_empty = smem_addr(sm.v_empty), s_full = smem_addr(sm.s_full),
@@ -792,7 +842,8 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
             mbar_arrive(q_full);
             const float f = a.scale * kLog2e * __int_as_float((127 - 14 + e) << 23);
             const int64_t seen = !in ? 0 : (a.causal ? (int64_t)q.len - q.n + tok + 1 : q.len);
-            const int vis = (int)max((int64_t)0, min(seen, (int64_t)q.len));
+            // from the first token of this range on
+            const int vis = (int)max((int64_t)0, min(seen, (int64_t)q.len)) - step0 * kKvTile;
 
             const uint32_t lanes = (uint32_t)(warp & 3) << 21;                // 32 lanes a warp, in bits 16 and up
             const uint32_t ts = tm_s + lanes + 128 * t, to = tm_o + lanes + D * t;
@@ -934,6 +985,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
             if (steps > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_full + 8 * t, 0, abort_flag));
             tc_fence_after();
             const int64_t at = (q.t0 + tok) * a.q_heads + head;
+            float *part = prompt_part<D>(parts, pair, split, range);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -944,6 +996,12 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
                 if (!in) continue;
+                if (ranges > 1) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(part + (128 * t + r) * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    continue;
+                }
                 uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + 32 * c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -954,7 +1012,10 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
                     dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
-            if (in && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2;
+            if (in && ranges > 1)
+                *reinterpret_cast<float2 *>(part + kPromptRows * D + 2 * (128 * t + r)) = make_float2(m, l);
+            else if (in && a.lse)
+                a.lse[at] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2;
         }
     } else if (warp < 12) {
         registers_down<104>();
@@ -972,7 +1033,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
         auto find = [&](int j) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int blk = j * 8 + 2 * w + i;
+                const int blk = (step0 + j) * 8 + 2 * w + i;
                 sc[i] = -1;
                 if (j < steps && blk < blocks) {
                     const int page = __ldg(pages + (blk >> bshift));
@@ -1118,6 +1179,64 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1) attn_prompt_kernel(const
     }
 }
 
+// The parts of the tile pairs that several CTAs shared, a warp for each row,
+// in the order of their ranges.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs a, int few_rows, int split,
+                                                                  float *parts) {
+    constexpr int V = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = a.c.heads, group = a.q_heads / H;
+    const int64_t pair = blockIdx.x / (kPromptRows / kJoinWarps);
+    const int r = (int)(blockIdx.x % (kPromptRows / kJoinWarps)) * kJoinWarps + warp, h = pair % H;
+    int slot;
+    const int b = find_slot(a, pair / H, slot);
+    PromptTile tile;
+    if (b < 0 || !prompt_tile(a, b, slot, few_rows, tile)) return;
+    const int ranges = prompt_ranges(tile.steps, split);
+    const int64_t row = tile.row0 + r;
+    if (ranges < 2 || row >= tile.rows) return;
+    const int64_t tok = row / group, at = (tile.q.t0 + tok) * a.q_heads + h * group + (row - tok * group);
+    // the ranges' maxima and sums: a lane each (kMostSplit <= 32)
+    float m = -INFINITY, l = 0.f;
+    if (lane < ranges) {
+        const float2 v = *(reinterpret_cast<const float2 *>(prompt_part<D>(parts, pair, split, lane) + kPromptRows * D) + r);
+        m = v.x;
+        l = v.y;
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // nothing seen in a range: no weight, unless its sum says NaN
+    const float w = m == -INFINITY ? (l == 0.f ? 0.f : l) : ex2(m - top);
+    float total = 0.f, x[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < ranges; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, l, i);
+        const float *src = prompt_part<D>(parts, pair, split, i) + r * D + lane * V;
+        float y[V];
+        if constexpr (V == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src);
+            y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(src);
+            y[0] = v.x, y[1] = v.y;
+        }
+        total = fmaf(wi, li, total);
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[k] = fmaf(wi, y[k], x[k]);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * D + lane * V);
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) dst[k] = pack_bf16x2(x[2 * k] * inv, x[2 * k + 1] * inv);
+    if (a.lse && lane == 0) a.lse[at] = total == 0.f ? -INFINITY : (top - kPBias + log2f(total)) * kLn2;
+}
+
 // Rows of a tile: 8 where a sequence has no more, 16 otherwise (the next tile of
 // the same head reads the cache again, mostly from L2).
 static int stream_tiles(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads) {
@@ -1125,10 +1244,45 @@ static int stream_tiles(int64_t tokens, int32_t batch, int32_t q_heads, int32_t 
     return rows <= 8 ? 1 : 2;
 }
 
-int64_t attn_kv8_workspace_bytes(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int sms) {
-    const int nt = stream_tiles(tokens, batch, q_heads, kv_heads);
-    const int64_t grid = (int64_t)sms * stream_ctas(nt), rows = 8 * nt;
-    return ((grid + 63) / 64 * 64 + 2 * grid * rows * (dim + 2)) * 4;
+static int64_t prompt_pairs(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads) {
+    return (tokens * (q_heads / kv_heads) / kPromptRows + batch) * kv_heads;
+}
+
+// CTAs to a tile pair: as many as the SMs have room for, no more than the
+// longest pass could feed.
+static int prompt_split(int64_t pairs, int64_t most_tokens, int sms) {
+    const int64_t room = sms / pairs, steps = (most_tokens + kKvTile - 1) / kKvTile;
+    const int64_t split = room < kMostSplit ? room : kMostSplit;
+    return prompt_ranges((int)(steps < 4096 ? steps : 4096), split < 1 ? 1 : (int)split);
+}
+
+// Which kernels a step takes.  A sequence's rows decide, on the device; what
+// the host can tell is the most rows that one may have, and for a single
+// sequence that they are all the step has.
+struct AttnPlan {
+    bool prompts, few;                // sequences of many rows, of few
+    int few_rows, nt, split;
+    int64_t stream_floats, pairs;
+};
+
+static AttnPlan attn_plan(const AttnArgs &a, int sms) {
+    AttnPlan p;
+    const int group = a.q_heads / a.c.heads;
+    p.prompts = (a.s.cu ? a.s.tokens : 1) * group > kFewRows;
+    p.few = !(p.prompts && a.s.batch == 1);
+    p.few_rows = p.few ? kFewRows : -1;
+    p.nt = stream_tiles(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
+    const int64_t grid = (int64_t)sms * stream_ctas(p.nt);
+    p.stream_floats = (grid + 63) / 64 * 64 + 2 * grid * (8 * p.nt) * (a.c.dim + 2);
+    p.pairs = prompt_pairs(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
+    p.split = p.prompts ? prompt_split(p.pairs, (int64_t)a.s.max_pages << a.s.page_shift, sms) : 1;
+    return p;
+}
+
+// Counters and parts of the streamed tiles, then parts of the tile pairs.
+int64_t attn_kv8_workspace_bytes(const AttnArgs &a, int sms) {
+    const AttnPlan p = attn_plan(a, sms);
+    return 4 * (p.stream_floats + (p.split > 1 ? p.pairs * p.split * kPromptRows * (a.c.dim + 2) : 0));
 }
 
 // Shared memory beyond the default, set once for a kernel and device.
@@ -1165,30 +1319,28 @@ static cudaError_t launch_stream(const AttnArgs &a, int few_rows, int sms, bool 
 }
 
 template <int D>
-static cudaError_t launch_prompt(const AttnArgs &a, int few_rows, cudaStream_t stream) {
+static cudaError_t launch_prompt(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream) {
     static bool done[64] = {};
     const int bytes = (int)sizeof(PromptSmem<D>) + 1024;
-    const cudaError_t e = allow_smem(attn_prompt_kernel<D>, bytes, done);
+    cudaError_t e = allow_smem(attn_prompt_kernel<D>, bytes, done);
     if (e != cudaSuccess) return e;
-    const int64_t slots = a.s.tokens * (a.q_heads / a.c.heads) / kPromptRows + a.s.batch;
-    attn_prompt_kernel<D><<<(unsigned)(slots * a.c.heads), kPromptWarps * 32, bytes, stream>>>(a, few_rows);
+    float *parts = static_cast<float *>(a.ws) + p.stream_floats;
+    attn_prompt_kernel<D><<<(unsigned)(p.pairs * p.split), kPromptWarps * 32, bytes, stream>>>(a, p.few_rows, p.split, parts);
+    if ((e = cudaGetLastError()) != cudaSuccess || p.split == 1) return e;
+    attn_join_kernel<D><<<(unsigned)(p.pairs * (kPromptRows / kJoinWarps)), kJoinWarps * 32, 0, stream>>>(a, p.few_rows, p.split, parts);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_kv8(const AttnArgs &a, int sms, cudaStream_t stream) {
-    // Which kernel a sequence takes is decided by its rows, on the device; what the host can tell is the most rows that
-    // one may have, and for a single sequence that they are all the step has.
-    const int64_t most = (a.s.cu ? a.s.tokens : 1) * (a.q_heads / a.c.heads);
-    const bool prompts = most > kFewRows;
-    const int few_rows = prompts && a.s.batch == 1 ? -1 : kFewRows;
-    if (prompts) {
-        const cudaError_t e = a.c.dim == 128 ? launch_prompt<128>(a, few_rows, stream) : launch_prompt<64>(a, few_rows, stream);
-        if (e != cudaSuccess || few_rows < 0) return e;
+    const AttnPlan p = attn_plan(a, sms);
+    if (p.prompts) {
+        const cudaError_t e = a.c.dim == 128 ? launch_prompt<128>(a, p, stream) : launch_prompt<64>(a, p, stream);
+        if (e != cudaSuccess || !p.few) return e;
     }
-    const int nt = stream_tiles(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
+    const bool beside = p.prompts && p.split == 1;   // directly behind attn_prompt_kernel
     if (a.c.dim == 128)
-        return nt == 1 ? launch_stream<128, 1>(a, kFewRows, sms, prompts, stream) : launch_stream<128, 2>(a, kFewRows, sms, prompts, stream);
-    return nt == 1 ? launch_stream<64, 1>(a, kFewRows, sms, prompts, stream) : launch_stream<64, 2>(a, kFewRows, sms, prompts, stream);
+        return p.nt == 1 ? launch_stream<128, 1>(a, kFewRows, sms, beside, stream) : launch_stream<128, 2>(a, kFewRows, sms, beside, stream);
+    return p.nt == 1 ? launch_stream<64, 1>(a, kFewRows, sms, beside, stream) : launch_stream<64, 2>(a, kFewRows, sms, beside, stream);
 }
 
 }  // namespace convrot

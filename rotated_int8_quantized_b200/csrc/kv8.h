@@ -86,6 +86,6 @@ cudaError_t launch_norm_rope(const NormRopeArgs &a, int sms, cudaStream_t stream
 cudaError_t launch_kv8_append(const AppendArgs &a, int sms, cudaStream_t stream);
 cudaError_t launch_kv8_read(const ReadArgs &a, int sms, cudaStream_t stream);
 cudaError_t launch_attn_kv8(const AttnArgs &a, int sms, cudaStream_t stream);
-int64_t attn_kv8_workspace_bytes(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int sms);
+int64_t attn_kv8_workspace_bytes(const AttnArgs &a, int sms);
 
 }  // namespace convrot

@@ -370,6 +370,24 @@ def test_attention_a_long_prompt(dim, hq, hk):
     _attend([1500], [777], hq, hk, dim, 64, rows=9, causal=False)
 
 
+@pytest.mark.parametrize("dim,hq,hk,lens,news", [
+    (128, 16, 2, [4000], [24]), (64, 6, 2, [3000, 130, 0, 2500], [60, 130, 0, 1]), (128, 8, 1, [257, 1030], [20, 33]),
+    (128, 40, 8, [2049], [13])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_short_prompts_on_long_contexts(dim, hq, hk, lens, news, causal):
+    """Few tile pairs: several CTAs share a pass and another kernel joins them."""
+    paged, q, out, lse, cu = _attend(lens, news, hq, hk, dim, 64, causal, rows=9)
+    for _ in range(5):
+        again, lse2 = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu, None, causal)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+    bad = q.clone()
+    bad[0, 1, 3] = float("nan")
+    out2, _ = cr.attn_kv8(bad, paged.cache, paged.table_dev, paged.kv_len, cu, None, causal)
+    hit = torch.zeros(out.shape[:2], dtype=torch.bool, device=DEV)
+    hit[0, 1] = True
+    assert out2[hit].isnan().all() and torch.equal(out2[~hit], out[~hit])
+
+
 def test_attention_mixes_prompts_and_single_tokens():
     _attend([900, 1, 400, 77, 0, 2000], [300, 1, 1, 1, 0, 1], 16, 2, 128, 64, rows=7)
 
