@@ -603,7 +603,8 @@ convrot_status_t convrot_qk_norm_rope(const convrot_qk_norm_rope_t *job, void *s
  * where one is needed, kv_len beyond max_pages * page_tokens, cu outside
  * 0 .. tokens) is recorded as CONVROT_ERR_INVALID_ARG for
  * convrot_device_status(); nothing is read or written out of bounds, tokens
- * on such pages are not stored, read as zeros and not attended to.
+ * on such pages are not stored, read as zeros and not attended to.  (A cu that
+ * decreases is out of contract, but stays in bounds too.)
  */
 typedef struct {
     const int32_t *page_table, *kv_len, *cu;
@@ -674,7 +675,9 @@ convrot_status_t convrot_kv8_read(const convrot_kv8_read_t *job, void *stream);
  *   out : BF16 [tokens, q_heads, head_dim] contiguous, overlaps no input
  *   scale : > 0, finite
  * Sums, maxima and accumulators are FP32; the weights of the value product
- * are FP16 (11 bits).  A non-finite query gives NaN in its own row only.
+ * are FP16 (11 bits).  Scores (scale * q . K) stay below 2^24 in magnitude:
+ * beyond that FP32 no longer tells neighbours apart.  A non-finite query gives
+ * NaN in its own row only.
  * Results do not depend on the order in which the GPU runs the work.
  * Workspace: convrot_attn_kv8_workspace_bytes (0 if the job is invalid),
  * zero-filled before first use, left zero-filled where it has to be.

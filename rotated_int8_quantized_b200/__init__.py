@@ -608,8 +608,9 @@ def _set_rows(job, name: str, t: Optional[torch.Tensor], heads: int, dim: int, t
     if not t.is_cuda or t.stride(2) != 1:
         raise ValueError("%s: expected a CUDA tensor whose rows are contiguous" % name)
     setattr(job, name, t.data_ptr())
-    setattr(job, name + "_token_stride", t.stride(0))
-    setattr(job, name + "_head_stride", t.stride(1))
+    # the stride of a single token or head means nothing
+    setattr(job, name + "_token_stride", t.stride(0) if tokens > 1 else 0)
+    setattr(job, name + "_head_stride", t.stride(1) if heads > 1 else 0)
 
 
 def _set_seqs(s: convrot_kv8_seqs_t, tokens: int, table: torch.Tensor, kv_len: torch.Tensor,
@@ -795,6 +796,8 @@ def kv8_append(q, k, v, cache: KV8Cache, page_table, kv_len, cu=None, q_weight=N
 
 def kv8_read(cache: KV8Cache, page_table, kv_len, tokens: Optional[int] = None, cu=None, stream=None):
     """KV8Read into new tensors of `tokens` rows (batch rows without cu)."""
+    if cu is not None and tokens is None:
+        raise ValueError("tokens: with cu the number of rows has to be given")
     shape = (tokens if cu is not None else page_table.shape[0], cache.handle.kv_heads, cache.handle.head_dim)
     with _allocating(stream, cache.k.device):
         k, v = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) for _ in "kv")

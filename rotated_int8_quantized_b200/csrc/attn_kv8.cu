@@ -126,7 +126,7 @@ __device__ __forceinline__ SeqInfo seq_info(const KvSeqs &s, int b) {
         t1 = __ldg(s.cu + b + 1);
     }
     const int64_t len = __ldg(s.kv_len + b), cap = (int64_t)s.max_pages << s.page_shift;
-    q.bad = t0 < 0 || t1 < t0 || t1 > s.tokens || len < 0 || len > cap;
+    q.bad = t0 < 0 || (b == 0 && t0 != 0) || t1 < t0 || t1 > s.tokens || len < 0 || len > cap;
     t0 = min(max(t0, (int64_t)0), s.tokens);
     t1 = min(max(t1, t0), s.tokens);
     q.t0 = t0;
@@ -144,8 +144,8 @@ __device__ __forceinline__ SeqInfo seq_info(const KvSeqs &s, int b) {
 // operand layout of mma.m16n8k16 (16 tokens x 16 dims of K as the first
 // operand, 16 dims x 16 tokens of V; the sums run over dims, then tokens, in an
 // order of our choosing, so a lane simply takes a quarter of a K row or an
-// eighth of a V row and queries and outputs follow the same order).  The next block is in flight
-// while one is worked on.
+// eighth of a V row and queries and outputs follow the same order).  The next
+// block's K is in flight from the moment this one's is used up, its V likewise.
 //
 // Bound by memory, so the cache's blocks are dealt out evenly: all units (64
 // tokens of a tile) of the step in one list, an equal range for each of the
@@ -763,7 +763,10 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
     }
     __syncthreads();
     const int b = sm.seq;
-    if (b < 0) return;
+    if (b < 0) {                                     // cu[0] > 0
+        if (tid == 0) report_invalid();
+        return;
+    }
     PromptTile tile;
     if (!prompt_tile(a, b, sm.slot, few_rows, tile)) return;
     const SeqInfo &q = tile.q;

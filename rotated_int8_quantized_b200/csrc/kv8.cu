@@ -81,7 +81,10 @@ __device__ __forceinline__ TokenPlace place_token(const KvSeqs &s, int64_t t) {
     const int b = search_lanes<L>(s.batch, t, [&](int i) { return (int64_t)__ldg(s.cu + i); });
     p.b = -1;
     p.pos = -1;
-    if (b < 0) return p;
+    if (b < 0) {                                     // cu[0] > 0
+        if ((threadIdx.x & (L - 1)) == 0) report_invalid();
+        return p;
+    }
     const int64_t end = __ldg(s.cu + b + 1);
     if (t >= end) return p;
     p.b = b;
@@ -390,7 +393,10 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
         j = 0;
     } else {
         b = search_lanes<L>(a.s.batch, slot, [&](int i) { return (int64_t)(__ldg(a.s.cu + i) >> 4) + 2 * (int64_t)i; });
-        if (b < 0) return;
+        if (b < 0) {                                 // cu[0] > 0
+            if (threadIdx.x == 0) report_invalid();
+            return;
+        }
         t0 = __ldg(a.s.cu + b);
         n = (int64_t)__ldg(a.s.cu + b + 1) - t0;
         j = slot - ((t0 >> 4) + 2 * (int64_t)b);

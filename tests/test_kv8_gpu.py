@@ -67,6 +67,17 @@ def test_norm_rope_many_heads_take_eight_rows_a_group():
         _near_bf16(y, ref, np.abs(ref).max(-1, keepdims=True))
 
 
+def test_single_rows_with_odd_strides():
+    """A view's stride along an axis of one means nothing."""
+    base = _randn(1, 3, 64)
+    q = base.as_strided((1, 3, 64), (5, 64, 1))
+    one = base[:, :1].as_strided((1, 1, 64), (7, 3, 1))
+    assert torch.equal(cr.qk_norm_rope(q, one)[0], base) and torch.equal(cr.qk_norm_rope(q, one)[1], base[:, :1])
+    paged = Paged([40], 3, 64, 16)
+    out, _ = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len)
+    assert torch.equal(out, cr.attn_kv8(base, paged.cache, paged.table_dev, paged.kv_len)[0])
+
+
 def test_norm_only_and_broadcast_input():
     q = _randn(1, 1, 64).expand(9, 3, 64)
     w = _randn(64, seed=2)
@@ -254,6 +265,11 @@ def test_append_bad_pages_are_recorded_and_skipped():
     # longer than its row of the table
     kv = torch.tensor([table.shape[1] * 16 + 5, 40], dtype=torch.int32, device=DEV)
     cr.kv8_append(None, k, v, paged.cache, paged.table_dev, kv, cu)
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+    # rows in front of the first sequence
+    cr.kv8_append(None, k, v, paged.cache, paged.table_dev, torch.tensor([40, 40], dtype=torch.int32, device=DEV),
+                  torch.tensor([32, 40, 80], dtype=torch.int32, device=DEV))
     with pytest.raises(cr.ConvrotError):
         cr.convrot_device_status()
     # cu that is no partition of the rows: recorded, nothing out of bounds
@@ -482,7 +498,7 @@ def test_attention_bad_device_arguments_are_recorded():
             assert torch.equal(out[news[0]:], good[news[0]:])
             with pytest.raises(cr.ConvrotError):
                 cr.convrot_device_status()
-        for bad in ([0, 10 ** 6, 10 ** 6], [0, sum(news), sum(news) - 1], [-4, 1, sum(news)]):
+        for bad in ([3, sum(news), sum(news)], [0, 10 ** 6, 10 ** 6], [0, sum(news), sum(news) - 1], [-4, 1, sum(news)]):
             cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, torch.tensor(bad, dtype=torch.int32, device=DEV))
             with pytest.raises(cr.ConvrotError):
                 cr.convrot_device_status()
@@ -544,6 +560,39 @@ def test_a_captured_step_follows_its_tensors(news):
         torch.cuda.synchronize()
         _check_attention(paged, rot, out, lse, news, True, dim ** -0.5, rows=4)
     cr.convrot_device_status()
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import subprocess
+    import sys
+    code = """
+import torch
+import rotated_int8_quantized_b200 as cr
+q = torch.randn(200, 8, 64, device="cuda").bfloat16()
+cache = cr.make_kv8_cache(20, 2, 64, 16)
+table = torch.arange(20, dtype=torch.int32, device="cuda").view(1, 20)
+kv = torch.tensor([200], dtype=torch.int32, device="cuda")
+cu = torch.tensor([0, 200], dtype=torch.int32, device="cuda")
+k = torch.randn(200, 2, 64, device="cuda").bfloat16()
+out, rot = torch.empty_like(q), torch.empty_like(q)
+append = cr.KV8Append(q, k, k, cache, table, kv, rot, cu=cu, rope=cr.Rope(cr.rope_table(300, 64)))
+attn = cr.AttnKV8(rot, cache, table, kv, out, cu=cu)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    append()
+    attn()
+g.replay()
+torch.cuda.synchronize()
+got = out.clone()
+append()
+attn()
+assert torch.equal(got, out) and out.abs().max() > 0
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=__import__("os").path.dirname(__import__("os").path.dirname(__import__("os").path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
 
 
 def test_two_streams_at_once():
