@@ -1031,31 +1031,39 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         const int bshift = S.page_shift - 4, bmask = (1 << bshift) - 1;
         const int blocks = (q.len + 15) >> 4;
         uint4 kx[4][DB], vx[4][DB];
-        int64_t sc[2];                               // the warp's two blocks of the tile in flight; -1: none
-        float ks[2], vs[2];
-        auto find = [&](int j) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int blk = (step0 + j) * 8 + 2 * w + i;
-                sc[i] = -1;
-                if (j < steps && blk < blocks) {
-                    const int page = __ldg(pages + (blk >> bshift));
-                    if (page >= 0 && page < S.pages)
-                        sc[i] = (((int64_t)page * H + h) << bshift) + (blk & bmask);
-                    else if (lane == 0)
-                        report_invalid();
-                }
+        // A lane looks after one of the warp's blocks of the next 16 steps: where it lies in the cache (-1: no token of it
+        // is seen) and what the rows' threads need of it.
+        int sc = -1;
+        float4 about = make_float4(0.f, -INFINITY, 0.f, 0.f);
+        auto look_up = [&](int j) {
+            const int step = j + (lane >> 1), blk = (step0 + step) * 8 + 2 * w + (lane & 1);
+            sc = -1;
+            about = make_float4(0.f, -INFINITY, 0.f, 0.f);
+            if (step >= steps || blk >= blocks) return;
+            const int page = __ldg(pages + (blk >> bshift));
+            if (page < 0 || page >= S.pages) {
+                report_invalid();
+                return;
             }
+            sc = ((page * H + h) << bshift) + (blk & bmask);
+            about.x = __ldg(a.c.ks + sc);
+            about.y = __ldg(a.c.vs + sc);            // until finish()
         };
-        auto load = [&](const int8_t *base, const float *scales, uint4 (&x)[4][DB], float (&s)[2]) {
+        auto finish = [&] {
+            if (sc < 0) return;
+            const float ve = fmaxf(about.y, kLeastScale);
+            about.y = log2f(ve);
+            about.z = 1.f / ve;
+        };
+        auto load = [&](const int8_t *base, int at, uint4 (&x)[4][DB]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                const int b = __shfl_sync(0xffffffffu, sc, 2 * at + (i >> 1));
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
-                    x[i][d] = sc[i >> 1] < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                                             : ld_stream16(base + sc[i >> 1] * (16 * D) + (8 * (i & 1) + rr) * D + 64 * d + 16 * c4);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) s[i] = sc[i] < 0 ? 0.f : __ldg(scales + sc[i]);
+                    x[i][d] = b < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                    : ld_stream16(base + (int64_t)b * (16 * D) + (8 * (i & 1) + rr) * D + 64 * d + 16 * c4);
+            }
         };
         auto store = [&](uint8_t (*dst)[128 * 128], const uint4 (&x)[4][DB]) {
 #pragma unroll
@@ -1073,35 +1081,35 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
                     *reinterpret_cast<uint4 *>(p + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                 }
         };
-        find(0);
-        load(a.c.k, a.c.ks, kx, ks);
-        load(a.c.v, a.c.vs, vx, vs);
+        look_up(0);
+        load(a.c.k, 0, kx);
+        load(a.c.v, 0, vx);
+        finish();
         for (int j = 0; j < steps; ++j) {
             const int st = j & 1;
             const uint32_t free_parity = ((j >> 1) & 1) ^ 1;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(k_empty + 8 * st, free_parity, abort_flag))) break;
             store(sm.k[st], kx);
-            if (lane < 2) {
-                const bool none = (lane ? sc[1] : sc[0]) < 0;
-                const float ve = fmaxf(lane ? vs[1] : vs[0], kLeastScale);
-                sm.info[j & (kInfoRing - 1)][2 * w + lane] =
-                    none ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                         : make_float4(lane ? ks[1] : ks[0], log2f(ve), 1.f / ve, 0.f);
-            }
+            const int mine = 2 * (j & 15) + (lane & 1);
+            const float4 now = make_float4(__shfl_sync(0xffffffffu, about.x, mine), __shfl_sync(0xffffffffu, about.y, mine),
+                                           __shfl_sync(0xffffffffu, about.z, mine), 0.f);
+            if (lane < 2) sm.info[j & (kInfoRing - 1)][2 * w + lane] = now;
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(k_full + 8 * st);
                 mbar_arrive(info_full + 8 * (j & (kInfoRing - 1)));
             }
-            find(j + 1);
-            load(a.c.k, a.c.ks, kx, ks);
+            const bool refill = ((j + 1) & 15) == 0;
+            if (refill) look_up(j + 1);
+            load(a.c.k, (j + 1) & 15, kx);
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(v_empty + 8 * st, free_parity, abort_flag))) break;
             store(sm.v[st], vx);
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_full + 8 * st);
-            load(a.c.v, a.c.vs, vx, vs);
+            load(a.c.v, (j + 1) & 15, vx);
+            if (refill) finish();
         }
     } else {
         registers_down<40>();
