@@ -31,9 +31,31 @@ constexpr int kStreamUnit = 16 * kStreamWarps;      // tokens a CTA takes at a t
 constexpr int kJoin = 64;                           // parts of a tile joined at a time
 constexpr float kPBias = 4.f;                       // p' is held times 2^4
 constexpr float kLazy = 11.f;                       // the running maximum moves once it is exceeded by 2^11
-// Sequences with at most so many rows (tokens times queries a key head) are
-// streamed, longer ones go through the tensor-core tiles.
-constexpr int kFewRows = 64;
+// Whether a sequence's rows (tokens times queries a key head) are streamed
+// (attn_stream_kernel) or go through tensor-core tiles (attn_prompt_kernel):
+// up to 64 rows always streamed, above 512 never.  Between,
+//   a sequence by itself goes by what either would take as measured at 64 / 8
+// heads of 128 and 40 / 40 of 64: the streaming kernel works off 230 (head dim
+// 64: 380) units of 16 rows x 64 tokens a microsecond after 4 us, the other
+// takes 10 us and 2 us a step of 128 tokens, eight at the most (several CTAs
+// share a pass).  96 rows on 512 tokens: 12.3 us streamed, 16.8 tiled; 512 rows
+// on 2048: 41.1 and 28.5.
+//   of several sequences all should go one way, or the step takes both times:
+// where sequences times key heads leave SMs idle and the rows average at most
+// 128, up to 256 are streamed.  Eight sequences at 8 key heads, up to 192 rows
+// on up to 1024 tokens: 34.3 us streamed, 48.4 partly tiled; up to 256 rows:
+// 54.7 and 34.7; at 40 key heads of 64, up to 128 rows: 62.7 and 50.8.
+constexpr int kFewRows = 64, kManyRows = 512;
+
+__host__ __device__ __forceinline__ bool few_rows(int64_t rows, int64_t len, const AttnArgs &a) {
+    if (rows <= kFewRows) return true;
+    if (rows > kManyRows) return false;
+    const int64_t heads = a.c.heads, batch = a.s.batch;
+    if (batch > 1) return rows <= 256 && batch * heads <= 148 && a.s.tokens * (a.q_heads / heads) <= 128 * batch;
+    const int64_t units = heads * ((rows + 15) / 16) * ((len + 63) / 64), steps = (len + 127) / 128;
+    return 4000 + units * (a.c.dim == 128 ? 4400 : 2600) / 1000 < 10000 + 2000 * (steps < 8 ? steps : 8);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Value scales below this count as this (a block of zeros has scale 0); the
@@ -166,7 +188,7 @@ struct StreamSmem {
 constexpr int stream_ctas(int nt) { return nt == 1 ? 4 : 2; }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a, int few_rows) {
+__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a, bool all) {
     constexpr int R = 8 * NT, T = kStreamWarps * 32;
     constexpr int VW = D / 32;                       // words of a V row a lane holds
     constexpr int MT = D / 16;                       // words of a K row a lane holds; 16-dim pieces of a row
@@ -179,7 +201,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
     // units of every sequence, summed; thread i holds sequences [i per, i per + per)
     const int per = (S.batch + T - 1) / T;
     auto seq_units = [&](const SeqInfo &q) {
-        if ((int64_t)q.n * group > few_rows) return 0ll;         // attn_prompt_kernel's
+        if (!all && !few_rows((int64_t)q.n * group, q.len, a)) return 0ll;       // attn_prompt_kernel's
         const int tiles = (q.n * group + R - 1) / R;
         const int units = q.len > 0 ? (q.len + kStreamUnit - 1) / kStreamUnit : 1;   // empty rows are written too
         return (long long)tiles * units * H;
@@ -617,14 +639,15 @@ constexpr int kPromptRows = 256;                     // two tiles
 constexpr int kKvTile = 128;
 constexpr int kInfoRing = 4;
 // Where there are too few tile pairs for the GPU, several CTAs share a pair's
-// pass over the cache, each a range of its steps (two at least), and leave FP32
-// sums and maxima in the workspace for attn_join_kernel: 192 rows on 8192
-// tokens at 8 key heads are 8 pairs, 64 steps each, for 148 SMs.
+// pass over the cache, each a range of its steps (four at least: the join costs
+// as much as three), and leave FP32 sums and maxima in the workspace for
+// attn_join_kernel: 192 rows on 8192 tokens at 8 key heads are 8 pairs, 64 steps
+// each, for 148 SMs.
 constexpr int kMostSplit = 16;
 
 // Ranges that a pass of `steps` is cut into, of `split` at the most.
 __host__ __device__ __forceinline__ int prompt_ranges(int steps, int split) {
-    const int n = steps / 2 < split ? steps / 2 : split;
+    const int n = steps / 4 < split ? steps / 4 : split;
     return n < 1 ? 1 : n;
 }
 
@@ -727,13 +750,13 @@ __device__ __forceinline__ int find_slot(const AttnArgs &a, int64_t slot, int &w
     return b;
 }
 
-__device__ __forceinline__ bool prompt_tile(const AttnArgs &a, int b, int slot, int few_rows, PromptTile &t) {
+__device__ __forceinline__ bool prompt_tile(const AttnArgs &a, int b, int slot, bool all, PromptTile &t) {
     const int group = a.q_heads / a.c.heads;
     t.b = b;
     t.q = seq_info(a.s, b);
     t.rows = (int64_t)t.q.n * group;
     t.row0 = (int64_t)slot * kPromptRows;
-    if (t.rows <= few_rows || t.row0 >= t.rows) return false;
+    if (t.row0 >= t.rows || (!all && few_rows(t.rows, t.q.len, a))) return false;
     // what the last row sees is what any row sees
     const int64_t tok = (min(t.rows, t.row0 + kPromptRows) - 1) / group;
     const int64_t most = a.causal ? max((int64_t)0, min((int64_t)t.q.len, (int64_t)t.q.len - t.q.n + tok + 1)) : t.q.len;
@@ -743,7 +766,7 @@ __device__ __forceinline__ bool prompt_tile(const AttnArgs &a, int b, int slot, 
 
 template <int D>
 __global__ void __launch_bounds__(kPromptWarps * 32, 1)
-    attn_prompt_kernel(const __grid_constant__ AttnArgs a, int few_rows, int split, float *parts) {
+    attn_prompt_kernel(const __grid_constant__ AttnArgs a, bool all, int split, float *parts) {
     constexpr int DB = D / 64;                       // 128-byte row blocks of an operand
     constexpr uint32_t kBlockBytes = 128 * 128;
     extern __shared__ uint8_t smem_raw[];
@@ -768,7 +791,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         return;
     }
     PromptTile tile;
-    if (!prompt_tile(a, b, sm.slot, few_rows, tile)) return;
+    if (!prompt_tile(a, b, sm.slot, all, tile)) return;
     const SeqInfo &q = tile.q;
     if (q.bad && tid == 0) report_invalid();
     const int64_t rows = tile.rows, row0 = tile.row0;
@@ -1195,7 +1218,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
 constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs a, int few_rows, int split,
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs a, bool all, int split,
                                                                   float *parts) {
     constexpr int V = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1205,7 +1228,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     int slot;
     const int b = find_slot(a, pair / H, slot);
     PromptTile tile;
-    if (b < 0 || !prompt_tile(a, b, slot, few_rows, tile)) return;
+    if (b < 0 || !prompt_tile(a, b, slot, all, tile)) return;
     const int ranges = prompt_ranges(tile.steps, split);
     const int64_t row = tile.row0 + r;
     if (ranges < 2 || row >= tile.rows) return;
@@ -1267,26 +1290,28 @@ static int prompt_split(int64_t pairs, int64_t most_tokens, int sms) {
     return prompt_ranges((int)(steps < 4096 ? steps : 4096), split < 1 ? 1 : (int)split);
 }
 
-// Which kernels a step takes.  A sequence's rows decide, on the device; what
-// the host can tell is the most rows that one may have, and for a single
-// sequence that they are all the step has.
+// Which kernels a step takes.  A sequence's rows and length decide, on the
+// device (few_rows); what the host can tell is the most rows that one may have
+// and how long the page table lets it be.  Where the largest is streamed, all
+// are: fewer rows never turn the rule, and in the length it holds a linear sum
+// that starts below against a concave one.
 struct AttnPlan {
-    bool prompts, few;                // sequences of many rows, of few
-    int few_rows, nt, split;
+    bool tiled, streamed;             // kernels to launch; with only one, it takes every sequence
+    int nt, split;
     int64_t stream_floats, pairs;
 };
 
 static AttnPlan attn_plan(const AttnArgs &a, int sms) {
     AttnPlan p;
     const int group = a.q_heads / a.c.heads;
-    p.prompts = (a.s.cu ? a.s.tokens : 1) * group > kFewRows;
-    p.few = !(p.prompts && a.s.batch == 1);
-    p.few_rows = p.few ? kFewRows : -1;
+    const int64_t most = (a.s.cu ? a.s.tokens : 1) * group, longest = (int64_t)a.s.max_pages << a.s.page_shift;
+    p.tiled = !few_rows(most, longest, a);
+    p.streamed = !(p.tiled && a.s.batch == 1 && most > kManyRows);
     p.nt = stream_tiles(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
     const int64_t grid = (int64_t)sms * stream_ctas(p.nt);
     p.stream_floats = (grid + 63) / 64 * 64 + 2 * grid * (8 * p.nt) * (a.c.dim + 2);
     p.pairs = prompt_pairs(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
-    p.split = p.prompts ? prompt_split(p.pairs, (int64_t)a.s.max_pages << a.s.page_shift, sms) : 1;
+    p.split = p.tiled ? prompt_split(p.pairs, longest, sms) : 1;
     return p;
 }
 
@@ -1311,7 +1336,7 @@ static cudaError_t allow_smem(Kernel *kernel, int bytes, bool (&done)[64]) {
 // start while that one's last CTAs run (it ends after them: a kernel that
 // follows on the stream finds both complete).
 template <int D, int NT>
-static cudaError_t launch_stream(const AttnArgs &a, int few_rows, int sms, bool beside, cudaStream_t stream) {
+static cudaError_t launch_stream(const AttnArgs &a, bool all, int sms, bool beside, cudaStream_t stream) {
     static bool done[64] = {};
     const int bytes = (int)sizeof(StreamSmem<D, NT>);
     const cudaError_t e = allow_smem(attn_stream_kernel<D, NT>, bytes, done);
@@ -1326,7 +1351,7 @@ static cudaError_t launch_stream(const AttnArgs &a, int few_rows, int sms, bool 
     cfg.stream = stream;
     cfg.attrs = beside ? attr : nullptr;
     cfg.numAttrs = beside ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_stream_kernel<D, NT>, a, few_rows);
+    return cudaLaunchKernelEx(&cfg, attn_stream_kernel<D, NT>, a, all);
 }
 
 template <int D>
@@ -1336,22 +1361,22 @@ static cudaError_t launch_prompt(const AttnArgs &a, const AttnPlan &p, cudaStrea
     cudaError_t e = allow_smem(attn_prompt_kernel<D>, bytes, done);
     if (e != cudaSuccess) return e;
     float *parts = static_cast<float *>(a.ws) + p.stream_floats;
-    attn_prompt_kernel<D><<<(unsigned)(p.pairs * p.split), kPromptWarps * 32, bytes, stream>>>(a, p.few_rows, p.split, parts);
+    attn_prompt_kernel<D><<<(unsigned)(p.pairs * p.split), kPromptWarps * 32, bytes, stream>>>(a, !p.streamed, p.split, parts);
     if ((e = cudaGetLastError()) != cudaSuccess || p.split == 1) return e;
-    attn_join_kernel<D><<<(unsigned)(p.pairs * (kPromptRows / kJoinWarps)), kJoinWarps * 32, 0, stream>>>(a, p.few_rows, p.split, parts);
+    attn_join_kernel<D><<<(unsigned)(p.pairs * (kPromptRows / kJoinWarps)), kJoinWarps * 32, 0, stream>>>(a, !p.streamed, p.split, parts);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_kv8(const AttnArgs &a, int sms, cudaStream_t stream) {
     const AttnPlan p = attn_plan(a, sms);
-    if (p.prompts) {
+    if (p.tiled) {
         const cudaError_t e = a.c.dim == 128 ? launch_prompt<128>(a, p, stream) : launch_prompt<64>(a, p, stream);
-        if (e != cudaSuccess || !p.few) return e;
+        if (e != cudaSuccess || !p.streamed) return e;
     }
-    const bool beside = p.prompts && p.split == 1;   // directly behind attn_prompt_kernel
+    const bool beside = p.tiled && p.split == 1;     // directly behind attn_prompt_kernel
     if (a.c.dim == 128)
-        return p.nt == 1 ? launch_stream<128, 1>(a, kFewRows, sms, beside, stream) : launch_stream<128, 2>(a, kFewRows, sms, beside, stream);
-    return p.nt == 1 ? launch_stream<64, 1>(a, kFewRows, sms, beside, stream) : launch_stream<64, 2>(a, kFewRows, sms, beside, stream);
+        return p.nt == 1 ? launch_stream<128, 1>(a, !p.tiled, sms, beside, stream) : launch_stream<128, 2>(a, !p.tiled, sms, beside, stream);
+    return p.nt == 1 ? launch_stream<64, 1>(a, !p.tiled, sms, beside, stream) : launch_stream<64, 2>(a, !p.tiled, sms, beside, stream);
 }
 
 }  // namespace convrot
