@@ -160,38 +160,87 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// Norm (if w) and rotation of a row's values, y[0..3] at g.a and y[4..7] at
-// g.b; the row's L lanes call it together.
-template <int L>
-__device__ __forceinline__ void norm_rotate(float (&y)[8], const float (&w)[8], bool norm, float eps, const LaneGeo &g,
-                                            bool adjacent, const float (&c)[4], const float (&s)[4]) {
-    if (norm) {
-        float q = 0.f;
+// A lane's eight values as FP32 pairs: the even and odd elements of its two
+// pieces, which is how they come apart from (and go back into) BF16 words.
+struct Row8 {
+    uint64_t e[2], o[2];                  // piece 0 (dims a ..): (0, 2) and (1, 3); piece 1 (dims b ..) likewise
+};
+
+__device__ __forceinline__ Row8 unpack_row(const uint2 &a, const uint2 &b) {
+    Row8 r;
+    r.e[0] = pack_f32x2(__uint_as_float(a.x << 16), __uint_as_float(a.y << 16));
+    r.o[0] = pack_f32x2(__uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y & 0xFFFF0000u));
+    r.e[1] = pack_f32x2(__uint_as_float(b.x << 16), __uint_as_float(b.y << 16));
+    r.o[1] = pack_f32x2(__uint_as_float(b.x & 0xFFFF0000u), __uint_as_float(b.y & 0xFFFF0000u));
+    return r;
+}
+
+__device__ __forceinline__ void row_piece(const Row8 &r, int piece, float (&y)[4]) {
+    unpack_f32x2(r.e[piece], y[0], y[2]);
+    unpack_f32x2(r.o[piece], y[1], y[3]);
+}
+
+__device__ __forceinline__ uint2 pack_piece(const Row8 &r, int piece) {
+    float y[4];
+    row_piece(r, piece, y);
+    return make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+}
+
+// What a row is multiplied by, the norm's weights and the rotation's
+// coefficients in one: with P and Q the two values of four rotated pairs (two
+// at a time), P' = P c1 - Q s1 and Q' = Q c2 + P s2, where c1 = w_P cos, s1 = w_Q
+// sin, c2 = w_Q cos, s2 = w_P sin.  P and Q are the pieces (Adjacent: the even
+// and odd elements of a piece).
+struct Turns {
+    uint64_t c1[2], s1[2], c2[2], s2[2];
+};
+
+template <bool Adjacent>
+__device__ __forceinline__ Turns make_turns(const float (&w)[8], const float (&c)[4], const float (&s)[4]) {
+    Turns t;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(y[i], y[i], q);
+    for (int k = 0; k < 2; ++k) {
+        // elements of P and Q, and their pairs' numbers
+        const int p0 = Adjacent ? 4 * k : k, q0 = Adjacent ? 4 * k + 1 : 4 + k, f0 = Adjacent ? 2 * k : k, f1 = Adjacent ? f0 + 1 : f0 + 2;
+        t.c1[k] = pack_f32x2(w[p0] * c[f0], w[p0 + 2] * c[f1]);
+        t.s1[k] = pack_f32x2(-w[q0] * s[f0], -w[q0 + 2] * s[f1]);
+        t.c2[k] = pack_f32x2(w[q0] * c[f0], w[q0 + 2] * c[f1]);
+        t.s2[k] = pack_f32x2(w[p0] * s[f0], w[p0 + 2] * s[f1]);
+    }
+    return t;
+}
+
+// Norm and rotation of a row; its L lanes call it together.
+template <int L, bool Adjacent>
+__device__ __forceinline__ void norm_rotate(Row8 &x, const Turns &t, bool norm, float eps) {
+    if (norm) {
+        uint64_t q = mul_f32x2(x.e[0], x.e[0]);
+        q = fma_f32x2(x.o[0], x.o[0], q);
+        q = fma_f32x2(x.e[1], x.e[1], q);
+        q = fma_f32x2(x.o[1], x.o[1], q);
+        float a, b;
+        unpack_f32x2(q, a, b);
+        a += b;
         // lanes of other rows of the warp may have left: only this row's take part
         const unsigned group = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) q += __shfl_xor_sync(group, q, o);
-        const float r = rsqrtf(q * (1.f / (8 * L)) + eps);
+        for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(group, a, o);
+        const float r = rsqrtf(fmaf(a, 1.f / (8 * L), eps));
+        const uint64_t r2 = pack_f32x2(r, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+        for (int k = 0; k < 2; ++k) x.e[k] = mul_f32x2(x.e[k], r2), x.o[k] = mul_f32x2(x.o[k], r2);
     }
-    if (!g.rotated) return;
-    if (adjacent) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u = y[2 * i], v = y[2 * i + 1];
-            y[2 * i] = u * c[i] - v * s[i];
-            y[2 * i + 1] = v * c[i] + u * s[i];
-        }
+    auto turn = [](uint64_t &p, uint64_t &q, const Turns &t, int k) {
+        const uint64_t u = fma_f32x2(q, t.s1[k], mul_f32x2(p, t.c1[k]));
+        q = fma_f32x2(p, t.s2[k], mul_f32x2(q, t.c2[k]));
+        p = u;
+    };
+    if (Adjacent) {
+        turn(x.e[0], x.o[0], t, 0);
+        turn(x.e[1], x.o[1], t, 1);
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u = y[i], v = y[4 + i];
-            y[i] = u * c[i] - v * s[i];
-            y[4 + i] = v * c[i] + u * s[i];
-        }
+        turn(x.e[0], x.e[1], t, 0);
+        turn(x.o[0], x.o[1], t, 1);
     }
 }
 
@@ -205,48 +254,49 @@ __device__ __forceinline__ void load_weight(const uint16_t *w, const LaneGeo &g,
     unpack_bf16x4(__ldg(reinterpret_cast<const uint2 *>(w + g.b)), out + 4);
 }
 
-// Heads [h0, h1) of token row t: load, norm, rotate, round, store, four rows
-// in flight and the next four behind them.  `rotation` fetches the
+// Heads [h0, h1) of token row t: load, norm, rotate, round, store, two rows at
+// a time and the next two in flight.  Bound by what it issues next to memory
+// (198 instructions a pair of rows one value at a time, 83 us for 8191 tokens of
+// 84 heads, 79% of the issue slots taken), hence the pairs.  `rotation` fetches the
 // coefficients (and says whether to write zeros) once the first rows are on
 // their way.  Rows may be rotated in place, so plain loads.
-template <int L, typename Rotation>
+template <int L, bool Adjacent, typename Rotation>
 __device__ __forceinline__ void head_rows(const HeadRows &in, const HeadRowsOut &out, int64_t t, int h0, int h1,
-                                          const uint16_t *weight, float eps, const LaneGeo &g, bool adjacent,
-                                          Rotation rotation) {
-    constexpr int U = 2;
-    const uint16_t *src = in.p + t * in.ts;
-    uint16_t *dst = out.p + t * out.ts;
-    uint2 x[U][2];
+                                          const uint16_t *weight, float eps, const LaneGeo &g, Rotation rotation) {
+    const uint16_t *src = in.p + t * in.ts + h0 * in.hs;
+    uint16_t *dst = out.p + t * out.ts + h0 * out.hs;
+    uint2 x[2][2];
     auto load = [&](int h) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (h + u < h1) {
-                x[u][0] = *reinterpret_cast<const uint2 *>(src + (h + u) * in.hs + g.a);
-                x[u][1] = *reinterpret_cast<const uint2 *>(src + (h + u) * in.hs + g.b);
-            }
+        if (h < h1) {
+            x[0][0] = *reinterpret_cast<const uint2 *>(src + g.a);
+            x[0][1] = *reinterpret_cast<const uint2 *>(src + g.b);
+        }
+        src += in.hs;
+        if (h + 1 < h1) {
+            x[1][0] = *reinterpret_cast<const uint2 *>(src + g.a);
+            x[1][1] = *reinterpret_cast<const uint2 *>(src + g.b);
+        }
+        src += in.hs;
     };
     load(h0);
     float w[8], c[4], s[4];
     load_weight(weight, g, w);
     const bool zero = !rotation(c, s);
-    for (int h = h0; h < h1; h += U) {
-        uint2 now[U][2];
+    const Turns turns = make_turns<Adjacent>(w, c, s);
+    for (int h = h0; h < h1; h += 2) {
+        Row8 y[2] = {unpack_row(x[0][0], x[0][1]), unpack_row(x[1][0], x[1][1])};
+        load(h + 2);
 #pragma unroll
-        for (int u = 0; u < U; ++u) now[u][0] = x[u][0], now[u][1] = x[u][1];
-        load(h + U);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < 2; ++u) {
             if (h + u < h1) {
-                float y[8];
-                unpack_bf16x4(now[u][0], y);
-                unpack_bf16x4(now[u][1], y + 4);
-                norm_rotate<L>(y, w, weight != nullptr, eps, g, adjacent, c, s);
-                uint2 lo = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-                uint2 hi = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                norm_rotate<L, Adjacent>(y[u], turns, weight != nullptr, eps);
+                uint2 lo = pack_piece(y[u], 0), hi = pack_piece(y[u], 1);
                 if (zero) lo = hi = make_uint2(0u, 0u);
-                *reinterpret_cast<uint2 *>(dst + (h + u) * out.hs + g.a) = lo;
-                *reinterpret_cast<uint2 *>(dst + (h + u) * out.hs + g.b) = hi;
+                *reinterpret_cast<uint2 *>(dst + g.a) = lo;
+                *reinterpret_cast<uint2 *>(dst + g.b) = hi;
             }
+            dst += out.hs;
+        }
     }
 }
 
@@ -256,7 +306,7 @@ __device__ __forceinline__ bool all_lanes(bool ok) {
     return __all_sync(group, ok);
 }
 
-template <int L>
+template <int L, bool Adjacent>
 __global__ void __launch_bounds__(kHeadThreads, 4) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per, int cq,
                                                                int chunks) {
     const int lane = threadIdx.x & (L - 1);
@@ -272,10 +322,10 @@ __global__ void __launch_bounds__(kHeadThreads, 4) norm_rope_kernel(const __grid
     };
     if (ch < cq) {
         const int h0 = ch * per;
-        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent, rotation);
+        head_rows<L, Adjacent>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, rotation);
     } else {
         const int h0 = (ch - cq) * per;
-        head_rows<L>(a.k, a.k_out, t, h0, min(h0 + per, a.kv_heads), a.kw, a.eps, g, a.rope.adjacent, rotation);
+        head_rows<L, Adjacent>(a.k, a.k_out, t, h0, min(h0 + per, a.kv_heads), a.kw, a.eps, g, rotation);
     }
 }
 
@@ -302,10 +352,9 @@ cudaError_t launch_norm_rope(const NormRopeArgs &a, int sms, cudaStream_t stream
     const int per = even(a.q_heads, heads_per_group(a.tokens, a.q_heads + a.kv_heads, L, sms));
     const int cq = (a.q_heads + per - 1) / per, chunks = cq + (a.kv_heads + per - 1) / per;
     const int64_t blocks = (a.tokens * chunks + kHeadThreads / L - 1) / (kHeadThreads / L);
-    if (L == 16)
-        norm_rope_kernel<16><<<(unsigned)blocks, kHeadThreads, 0, stream>>>(a, per, cq, chunks);
-    else
-        norm_rope_kernel<8><<<(unsigned)blocks, kHeadThreads, 0, stream>>>(a, per, cq, chunks);
+    const auto kernel = L == 16 ? (a.rope.adjacent ? norm_rope_kernel<16, true> : norm_rope_kernel<16, false>)
+                                : (a.rope.adjacent ? norm_rope_kernel<8, true> : norm_rope_kernel<8, false>);
+    kernel<<<(unsigned)blocks, kHeadThreads, 0, stream>>>(a, per, cq, chunks);
     return cudaGetLastError();
 }
 
@@ -352,7 +401,7 @@ __device__ __forceinline__ float grow_scale(float most, bool held, float old, fl
 
 // CTA = 16 rows x L lanes: one block of 16 tokens of one head, keys and
 // values together (blockIdx.x < kv_ctas), or chunks of the queries' heads.
-template <int L>
+template <int L, bool Adjacent>
 __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid_constant__ AppendArgs a, int64_t kv_ctas, int per,
                                                           int chunks) {
     const int lane = threadIdx.x & (L - 1), row = threadIdx.x / L;
@@ -366,7 +415,7 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
         const TokenPlace p = place_token<L>(a.s, t);
         if (p.b < 0) return;
         const int h0 = (int)(task - t * chunks) * per;
-        head_rows<L>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g, a.rope.adjacent,
+        head_rows<L, Adjacent>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g,
                      [&](float (&c)[4], float (&s)[4]) {
 #pragma unroll
                          for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
@@ -421,7 +470,7 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
     const bool held = blk * kKvBlock < first;               // the block has older tokens
     const int64_t t = t0 + n - (len - pos);
     // the row's values and coefficients are on their way before the page is known
-    float k[8], v[8], w[8], c[4], s[4], mk = 0.f, mv = 0.f;
+    float k[2][4], v[2][4], w[8], c[4], s[4], mk = 0.f, mv = 0.f;
     uint2 x[4];
     bool ok = true;
     if (fresh) {
@@ -440,18 +489,20 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
     const float old_k = held ? a.c.ks[sc] : 0.f, old_v = held ? a.c.vs[sc] : 0.f;
     if (fresh) {
         ok = all_lanes<L>(ok);
-        unpack_bf16x4(x[0], k);
-        unpack_bf16x4(x[1], k + 4);
-        unpack_bf16x4(x[2], v);
-        unpack_bf16x4(x[3], v + 4);
-        norm_rotate<L>(k, w, a.kw != nullptr, a.eps, g, a.rope.adjacent, c, s);
-        if (!ok) {
-            if (lane == 0) report_invalid();
+        Row8 y = unpack_row(x[0], x[1]);
+        norm_rotate<L, Adjacent>(y, make_turns<Adjacent>(w, c, s), a.kw != nullptr, a.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) k[i] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+            row_piece(y, i, k[i]);
+            unpack_bf16x4(x[2 + i], v[i]);
         }
+        if (!ok && lane == 0) report_invalid();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mk = fmaxf(mk, fabsf(k[i])), mv = fmaxf(mv, fabsf(v[i]));
+        for (int i = 0; i < 8; ++i) {
+            if (!ok) k[i >> 2][i & 3] = 0.f;
+            mk = fmaxf(mk, fabsf(k[i >> 2][i & 3]));
+            mv = fmaxf(mv, fabsf(v[i >> 2][i & 3]));
+        }
     }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) {
@@ -468,10 +519,10 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
     const int64_t at = (sc * kKvBlock + row) * a.c.dim;
     int8_t *kq = a.c.k + at, *vq = a.c.v + at;
     if (fresh) {
-        *reinterpret_cast<uint32_t *>(kq + g.a) = codes4(k, sk);
-        *reinterpret_cast<uint32_t *>(kq + g.b) = codes4(k + 4, sk);
-        *reinterpret_cast<uint32_t *>(vq + g.a) = codes4(v, sv);
-        *reinterpret_cast<uint32_t *>(vq + g.b) = codes4(v + 4, sv);
+        *reinterpret_cast<uint32_t *>(kq + g.a) = codes4(k[0], sk);
+        *reinterpret_cast<uint32_t *>(kq + g.b) = codes4(k[1], sk);
+        *reinterpret_cast<uint32_t *>(vq + g.a) = codes4(v[0], sv);
+        *reinterpret_cast<uint32_t *>(vq + g.b) = codes4(v[1], sv);
     } else if (pos < first) {
         if (shrink_k != 1.f) {
             uint2 *p = reinterpret_cast<uint2 *>(kq + 8 * lane);
@@ -494,10 +545,9 @@ cudaError_t launch_kv8_append(const AppendArgs &a, int sms, cudaStream_t stream)
     const int per = even(a.q_heads, heads_per_group(a.s.tokens, a.q_heads, L, sms));
     const int chunks = (a.q_heads + per - 1) / per;
     const int64_t blocks = kv_ctas + (a.s.tokens * chunks + 15) / 16;
-    if (L == 16)
-        kv8_append_kernel<16><<<(unsigned)blocks, 16 * 16, 0, stream>>>(a, kv_ctas, per, chunks);
-    else
-        kv8_append_kernel<8><<<(unsigned)blocks, 16 * 8, 0, stream>>>(a, kv_ctas, per, chunks);
+    const auto kernel = L == 16 ? (a.rope.adjacent ? kv8_append_kernel<16, true> : kv8_append_kernel<16, false>)
+                                : (a.rope.adjacent ? kv8_append_kernel<8, true> : kv8_append_kernel<8, false>);
+    kernel<<<(unsigned)blocks, 16 * L, 0, stream>>>(a, kv_ctas, per, chunks);
     return cudaGetLastError();
 }
 
