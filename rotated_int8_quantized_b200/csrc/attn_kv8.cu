@@ -23,6 +23,7 @@
 
 #include "common.cuh"
 #include "kv8.h"
+#include "umma_f16.cuh"
 
 namespace convrot {
 
@@ -175,6 +176,15 @@ __device__ __forceinline__ SeqInfo seq_info(const KvSeqs &s, int b) {
 // parts (FP32 sums, maximum) in the workspace, and the CTA that finds itself
 // last at the tile's counter joins them, in the order of the ranges, and sets
 // the counter back to zero.
+//
+// Measured at 64 / 8 heads of 128: 64 sequences of 2048 .. 8192 tokens (675 MB)
+// 134 .. 140 us, 3 of up to 131071 (694 MB) 136 .. 142 us, 75 .. 78 % of the copy
+// rate; with the products left out the loads alone take 124 us, so about a
+// third of the rest is conversion (some 300 instructions a block and warp) and
+// the rest the start (5 us to the first block) and the join (4 us).  Four CTAs
+// of 128 registers an SM beat three with the next block in registers (147 us)
+// and five with spills (157 us); bulk prefetch into L2 five blocks ahead cost 9
+// us, 16- or 32-byte loads of K made no difference.
 template <int D, int NT>
 struct StreamSmem {
     float o[kStreamWarps][8 * NT][D + 4];            // later the maxima and sums of a tile's parts, [kJoin][8 NT][2]
@@ -187,8 +197,10 @@ struct StreamSmem {
 // CTAs of the persistent grid on an SM; also what the registers are held to.
 constexpr int stream_ctas(int nt) { return nt == 1 ? 4 : 2; }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a, bool all) {
+// All: every sequence is this kernel's (the rule between the two kernels would
+// cost a tile of 8 rows registers that it does not have: 96 bytes of spills, 6 us of 134).
+template <int D, int NT, bool All>
+__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_stream_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int R = 8 * NT, T = kStreamWarps * 32;
     constexpr int VW = D / 32;                       // words of a V row a lane holds
     constexpr int MT = D / 16;                       // words of a K row a lane holds; 16-dim pieces of a row
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
     // units of every sequence, summed; thread i holds sequences [i per, i per + per)
     const int per = (S.batch + T - 1) / T;
     auto seq_units = [&](const SeqInfo &q) {
-        if (!all && !few_rows((int64_t)q.n * group, q.len, a)) return 0ll;       // attn_prompt_kernel's
+        if (!All && !few_rows((int64_t)q.n * group, q.len, a)) return 0ll;       // attn_prompt_kernel's
         const int tiles = (q.n * group + R - 1) / R;
         const int units = q.len > 0 ? (q.len + kStreamUnit - 1) / kStreamUnit : 1;   // empty rows are written too
         return (long long)tiles * units * H;
@@ -630,6 +642,16 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
 // the tensor cores work on the other.
 // K and V tiles are the same rows of 128 bytes (64 dims) in the 128-byte
 // swizzle; K is read along the dims (K-major), V along the tokens (MN-major).
+// Measured at 64 / 8 heads of 128: a prompt of 8192 tokens 1.19 .. 1.23 ms, 890 ..
+// 926 TFLOP/s of what is visible (55 % of the cuBLAS rate).  Of a step's 3850
+// clocks a tile spends 2100 in its softmax (of which 1024 are the exponentials'
+// at 8 clocks a warp and instruction; two warps at once would need 1275 each),
+// 1330 in its two products (1024 at full rate; the operands of Q K^T alone take
+// all of the shared memory's bandwidth) and 400 between them, and the other tile
+// fills the tensor cores only meanwhile: a second S buffer would decouple the
+// two, but tensor memory is full at head dim 128.  Measured and dropped: two
+// threads a row (1.45 ms: barriers and register spills), the maximum in a pass
+// of its own (1.39 ms), a branch for every 32 columns (1.27 ms).
 // The blocks' scales go through a ring of four, so that a step's are still
 // there, and its barrier's phase still open to be seen, whatever the order in
 // which the warps get on: step j + 4's are written after S of step j + 2,
@@ -1335,11 +1357,11 @@ static cudaError_t allow_smem(Kernel *kernel, int bytes, bool (&done)[64]) {
 // beside: launched behind attn_prompt_kernel and independent of it, so it may
 // start while that one's last CTAs run (it ends after them: a kernel that
 // follows on the stream finds both complete).
-template <int D, int NT>
-static cudaError_t launch_stream(const AttnArgs &a, bool all, int sms, bool beside, cudaStream_t stream) {
+template <int D, int NT, bool All>
+static cudaError_t launch_stream(const AttnArgs &a, int sms, bool beside, cudaStream_t stream) {
     static bool done[64] = {};
     const int bytes = (int)sizeof(StreamSmem<D, NT>);
-    const cudaError_t e = allow_smem(attn_stream_kernel<D, NT>, bytes, done);
+    const cudaError_t e = allow_smem(attn_stream_kernel<D, NT, All>, bytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -1351,7 +1373,15 @@ static cudaError_t launch_stream(const AttnArgs &a, bool all, int sms, bool besi
     cfg.stream = stream;
     cfg.attrs = beside ? attr : nullptr;
     cfg.numAttrs = beside ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_stream_kernel<D, NT>, a, all);
+    return cudaLaunchKernelEx(&cfg, attn_stream_kernel<D, NT, All>, a);
+}
+
+template <int D>
+static cudaError_t launch_stream(const AttnArgs &a, const AttnPlan &p, int sms, cudaStream_t stream) {
+    const bool beside = p.tiled && p.split == 1;     // directly behind attn_prompt_kernel
+    if (p.nt == 1)
+        return p.tiled ? launch_stream<D, 1, false>(a, sms, beside, stream) : launch_stream<D, 1, true>(a, sms, beside, stream);
+    return p.tiled ? launch_stream<D, 2, false>(a, sms, beside, stream) : launch_stream<D, 2, true>(a, sms, beside, stream);
 }
 
 template <int D>
@@ -1373,10 +1403,7 @@ cudaError_t launch_attn_kv8(const AttnArgs &a, int sms, cudaStream_t stream) {
         const cudaError_t e = a.c.dim == 128 ? launch_prompt<128>(a, p, stream) : launch_prompt<64>(a, p, stream);
         if (e != cudaSuccess || !p.streamed) return e;
     }
-    const bool beside = p.tiled && p.split == 1;     // directly behind attn_prompt_kernel
-    if (a.c.dim == 128)
-        return p.nt == 1 ? launch_stream<128, 1>(a, !p.tiled, sms, beside, stream) : launch_stream<128, 2>(a, !p.tiled, sms, beside, stream);
-    return p.nt == 1 ? launch_stream<64, 1>(a, !p.tiled, sms, beside, stream) : launch_stream<64, 2>(a, !p.tiled, sms, beside, stream);
+    return a.c.dim == 128 ? launch_stream<128>(a, p, sms, stream) : launch_stream<64>(a, p, sms, stream);
 }
 
 }  // namespace convrot
