@@ -356,7 +356,7 @@ LENS = [1, 0, 15, 16, 17, 63, 64, 65, 129, 700]
 
 
 @pytest.mark.parametrize("dim,hq,hk,page", [(128, 8, 1, 64), (128, 8, 8, 16), (64, 12, 4, 32), (64, 16, 1, 256),
-                                            (128, 10, 2, 128), (128, 40, 2, 64)])
+                                            (128, 10, 2, 128), (128, 40, 2, 64), (64, 128, 1, 1024), (128, 100, 1, 16)])
 def test_attention_single_tokens(dim, hq, hk, page):
     _attend(LENS, [1] * len(LENS), hq, hk, dim, page, cu=False)
 
@@ -406,6 +406,27 @@ def test_attention_short_prompts_on_long_contexts(dim, hq, hk, lens, news, causa
 
 def test_attention_mixes_prompts_and_single_tokens():
     _attend([900, 1, 400, 77, 0, 2000], [300, 1, 1, 1, 0, 1], 16, 2, 128, 64, rows=7)
+
+
+def test_many_sequences():
+    """More sequences than lanes or threads: every search and sum over them takes several rounds."""
+    g = torch.Generator().manual_seed(3)
+    batch, hk, dim = 1100, 1, 64
+    lens = torch.randint(0, 40, (batch,), generator=g).tolist()
+    news = [min(n, int(r)) for n, r in zip(lens, torch.randint(0, 4, (batch,), generator=g))]
+    paged, q, out, lse, cu = _attend(lens, news, 2, hk, dim, 16)
+    # all single tokens, 128 rows each: too many for the streaming kernel's rule
+    _attend([n + 1 for n in lens[:170]], [1] * 170, 128, 1, 64, 16, cu=False)
+    # the same sequences appended to and read back
+    old = [n - m for n, m in zip(lens, news)]
+    roomy = _roomy(old, lens, hk, dim, 16)
+    _, k, v, _, old, before = _append(roomy, news, 0, hk, dim, 5)
+    _check_append(roomy, news, bits_to_f64(k), bits_to_f64(v), old, before)
+    kb, vb = cr.kv8_read(roomy.cache, roomy.table_dev, roomy.kv_len, sum(news), cu)
+    for which, got in ((0, kb), (1, vb)):
+        ref = np.concatenate([roomy.values(b, which)[lens[b] - m:] for b, m in enumerate(news)])
+        assert (np.abs(bits_to_f64(got) - ref) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(ref)).all()
+    cr.convrot_device_status()
 
 
 def test_attention_rows_before_the_sequence_see_nothing():
