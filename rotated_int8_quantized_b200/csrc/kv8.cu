@@ -258,9 +258,9 @@ __device__ __forceinline__ void load_weight(const uint16_t *w, const LaneGeo &g,
 // a time and the next two in flight.  Next to memory it is bound by what it
 // issues (one value at a time: 198 instructions a pair of rows, 79 % of the issue
 // slots, 83 us for 8191 tokens of 84 heads), hence the FP32 pairs: 75 us, 4.75
-// TB/s, 73 % of the copy rate.  `rotation` fetches the
-// coefficients (and says whether to write zeros) once the first rows are on
-// their way.  Rows may be rotated in place, so plain loads.
+// TB/s, 73 % of the copy rate.  `rotation` finds the coefficients once the first
+// rows are on their way, and says what to write: the rows (1), zeros (0) or
+// nothing (-1).  Rows may be rotated in place, so plain loads.
 template <int L, bool Adjacent, typename Rotation>
 __device__ __forceinline__ void head_rows(const HeadRows &in, const HeadRowsOut &out, int64_t t, int h0, int h1,
                                           const uint16_t *weight, float eps, const LaneGeo &g, Rotation rotation) {
@@ -282,7 +282,8 @@ __device__ __forceinline__ void head_rows(const HeadRows &in, const HeadRowsOut 
     load(h0);
     float w[8], c[4], s[4];
     load_weight(weight, g, w);
-    const bool zero = !rotation(c, s);
+    const int what = rotation(c, s);
+    if (what < 0) return;
     const Turns turns = make_turns<Adjacent>(w, c, s);
     for (int h = h0; h < h1; h += 2) {
         Row8 y[2] = {unpack_row(x[0][0], x[0][1]), unpack_row(x[1][0], x[1][1])};
@@ -292,7 +293,7 @@ __device__ __forceinline__ void head_rows(const HeadRows &in, const HeadRowsOut 
             if (h + u < h1) {
                 norm_rotate<L, Adjacent>(y[u], turns, weight != nullptr, eps);
                 uint2 lo = pack_piece(y[u], 0), hi = pack_piece(y[u], 1);
-                if (zero) lo = hi = make_uint2(0u, 0u);
+                if (what == 0) lo = hi = make_uint2(0u, 0u);
                 *reinterpret_cast<uint2 *>(dst + g.a) = lo;
                 *reinterpret_cast<uint2 *>(dst + g.b) = hi;
             }
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kHeadThreads, 4) norm_rope_kernel(const __grid
     auto rotation = [&](float (&c)[4], float (&s)[4]) {
         const bool ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.tokens, -1, c, s));
         if (!ok && lane == 0) report_invalid();
-        return ok;
+        return ok ? 1 : 0;
     };
     if (ch < cq) {
         const int h0 = ch * per;
@@ -413,17 +414,17 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
         const int64_t task = ((int64_t)blockIdx.x - kv_ctas) * 16 + row;
         const int64_t t = task / chunks;
         if (t >= a.s.tokens) return;
-        const TokenPlace p = place_token<L>(a.s, t);
-        if (p.b < 0) return;
         const int h0 = (int)(task - t * chunks) * per;
         head_rows<L, Adjacent>(a.q, a.q_out, t, h0, min(h0 + per, a.q_heads), a.qw, a.eps, g,
                      [&](float (&c)[4], float (&s)[4]) {
 #pragma unroll
                          for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
-                         if (p.pos < 0) return false;                       // padding: zeros
+                         const TokenPlace p = place_token<L>(a.s, t);
+                         if (p.b < 0) return -1;                            // behind the last sequence
+                         if (p.pos < 0) return 0;                           // padding: zeros
                          const bool ok = all_lanes<L>(load_rotation(a.rope, g, lane, t, a.s.tokens, p.pos, c, s)) && p.pos < cap;
                          if (!ok && lane == 0) report_invalid();
-                         return ok;
+                         return ok ? 1 : 0;
                      });
         return;
     }
