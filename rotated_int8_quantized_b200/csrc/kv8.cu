@@ -361,8 +361,21 @@ cudaError_t launch_norm_rope(const NormRopeArgs &a, int sms, cudaStream_t stream
 }
 
 // ------------------------------------------------------------ append
-// Codes of a lane's eight values on scale s (0: an all-zero block).
-__device__ __forceinline__ uint32_t codes4(const float *y, float s) {
+// Four codes on scale s (0: an all-zero block): clamp(rne(fl(y / s))).  The
+// quotient itself is only needed near a half: with r = fl(1 / s), y r is within
+// |y / s| 2^-22 < 3.1e-5 of it (|y / s| <= 127.5), so an integer that y r is less
+// than 0.4999 from is the quotient's nearest.
+__device__ __forceinline__ uint32_t codes4(const float *y, float s, float r) {
+    constexpr float kMagic = 12582912.f;          // 1.5 * 2^23: the sum's low byte is the integer
+    float e[4], off = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        e[i] = fmaf(y[i], r, kMagic);
+        off = fmaxf(off, fabsf(fmaf(y[i], r, kMagic - e[i])));
+    }
+    // r: zero where 1 / s is no normal number
+    if (r != 0.f && off < 0.4999f)
+        return pack_low_bytes(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -371,6 +384,10 @@ __device__ __forceinline__ uint32_t codes4(const float *y, float s) {
         w |= ((uint32_t)(int)q & 0xFFu) << (8 * i);
     }
     return w;
+}
+
+__device__ __forceinline__ float code_factor(float s) {
+    return s >= 1.17549435e-38f && s <= 8.5e37f ? __frcp_rn(s) : 0.f;
 }
 
 // rne(q * f) of four codes; f = 2^-j (or 0), so the product is exact.
@@ -521,10 +538,11 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
     const int64_t at = (sc * kKvBlock + row) * a.c.dim;
     int8_t *kq = a.c.k + at, *vq = a.c.v + at;
     if (fresh) {
-        *reinterpret_cast<uint32_t *>(kq + g.a) = codes4(k[0], sk);
-        *reinterpret_cast<uint32_t *>(kq + g.b) = codes4(k[1], sk);
-        *reinterpret_cast<uint32_t *>(vq + g.a) = codes4(v[0], sv);
-        *reinterpret_cast<uint32_t *>(vq + g.b) = codes4(v[1], sv);
+        const float rk = code_factor(sk), rv = code_factor(sv);
+        *reinterpret_cast<uint32_t *>(kq + g.a) = codes4(k[0], sk, rk);
+        *reinterpret_cast<uint32_t *>(kq + g.b) = codes4(k[1], sk, rk);
+        *reinterpret_cast<uint32_t *>(vq + g.a) = codes4(v[0], sv, rv);
+        *reinterpret_cast<uint32_t *>(vq + g.b) = codes4(v[1], sv, rv);
     } else if (pos < first) {
         if (shrink_k != 1.f) {
             uint2 *p = reinterpret_cast<uint2 *>(kq + 8 * lane);
