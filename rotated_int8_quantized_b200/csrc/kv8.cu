@@ -530,9 +530,13 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
     }
     if (lane == 0) most_k[row] = mk, most_v[row] = mv;
     __syncthreads();
-    mk = mv = 0.f;
+    mk = most_k[threadIdx.x & 15];
+    mv = most_v[threadIdx.x & 15];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mk = fmaxf(mk, most_k[i]), mv = fmaxf(mv, most_v[i]);
+    for (int o = 8; o > 0; o >>= 1) {
+        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
     float shrink_k, shrink_v;
     const float sk = grow_scale(mk, held, old_k, shrink_k), sv = grow_scale(mv, held, old_v, shrink_v);
     const int64_t at = (sc * kKvBlock + row) * a.c.dim;

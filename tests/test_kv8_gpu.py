@@ -210,6 +210,26 @@ def test_append_token_by_token_stays_within_a_step():
     cr.convrot_device_status()
 
 
+def test_append_ties_go_to_even_and_the_scale_doubles_at_127_and_a_half():
+    hk, dim = 1, 64
+    row = torch.zeros(64)
+    row[:16] = torch.tensor([127.0, 0.5, 1.5, 2.5, -0.5, -1.5, -2.5, 3.5, 20.5, 21.5, -40.5, 63.5, -127.0, 1.0, 0.25, 126.0])
+    x = row.bfloat16().view(1, hk, dim).to(DEV)
+    for second, scale in ((127.0, 1.0), (127.5, 2.0), (255.0, 4.0), (254.0, 2.0)):
+        paged = _roomy([0], [16], hk, dim, 16)
+        _append(paged, [1], 0, hk, dim, 0, cu=None, k=x, v=x)
+        page = int(paged.table[0, 0])
+        assert float(paged.cache.v_scale[page, 0, 0]) == 1.0
+        assert paged.cache.v[page, 0, 0, :16].tolist() == [127, 0, 2, 2, 0, -2, -2, 4, 20, 22, -40, 64, -127, 1, 0, 126]
+        y = torch.zeros_like(x)
+        y[..., 0] = second
+        _append(paged, [1], 0, hk, dim, 0, cu=None, k=x, v=y)
+        assert float(paged.cache.v_scale[page, 0, 0]) == scale
+        first = np.array([127, 0, 2, 2, 0, -2, -2, 4, 20, 22, -40, 64, -127, 1, 0, 126], dtype=np.float64)
+        assert paged.cache.v[page, 0, 0, :16].tolist() == np.rint(first / scale).tolist()
+        assert int(paged.cache.v[page, 0, 1, 0]) == min(127, round(second / scale))
+
+
 def test_append_after_a_block_of_zeros_and_far_larger_values():
     hk, dim = 1, 64
     paged = _roomy([0], [16], hk, dim, 16)
