@@ -680,7 +680,11 @@ convrot_status_t convrot_kv8_read(const convrot_kv8_read_t *job, void *stream);
  * NaN in its own row only.
  * Results do not depend on the order in which the GPU runs the work.
  * Workspace: convrot_attn_kv8_workspace_bytes (0 if the job is invalid),
- * zero-filled before first use, left zero-filled where it has to be.
+ * zero-filled before first use.  Every call leaves the counters at its front
+ * zero again and sums of its own behind them, so attention calls of any shapes
+ * may follow one another on one workspace of the largest one's size; calls
+ * that may run at the same time need one each, and so do the other entry
+ * points (they expect all of theirs zero).
  */
 typedef struct {
     const convrot_kv8_t *cache;

@@ -735,8 +735,9 @@ class AttnKV8(_Prepared):
     """Attention of q [tokens, q_heads, head_dim] over the cache into out
     (contiguous, BF16) and, if given, lse [tokens, q_heads] (fp32).  The
     rows of sequence b are its last cu[b + 1] - cu[b] tokens.  ws: a
-    zero-filled workspace of at least `ws_bytes`, which calls that run at the
-    same time must not share (allocated here if None)."""
+    workspace of at least `ws_bytes`, zero-filled before its first call
+    (allocated here if None); AttnKV8 calls of any shapes may share one, but
+    neither calls that run at the same time nor the linears' calls."""
     _entry = "convrot_attn_kv8"
 
     def __init__(self, q, cache: KV8Cache, page_table, kv_len, out, cu=None, lse=None, scale: Optional[float] = None,

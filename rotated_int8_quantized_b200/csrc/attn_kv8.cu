@@ -195,7 +195,15 @@ struct StreamSmem {
 };
 
 // CTAs of the persistent grid on an SM; also what the registers are held to.
-constexpr int stream_ctas(int nt) { return nt == 1 ? 4 : 2; }
+constexpr int kMostStreamCtas = 4;
+__host__ __device__ constexpr int stream_ctas(int nt) { return nt == 1 ? kMostStreamCtas : 2; }
+
+// Tile counters in front of the workspace, as many as the larger grid needs
+// whichever is launched: calls of other shapes on the same workspace leave
+// sums behind them, never in them.
+__host__ __device__ constexpr int stream_counters(int grid, int nt) {
+    return (grid / stream_ctas(nt) * kMostStreamCtas + 63) / 64 * 64;
+}
 
 // All: every sequence is this kernel's (the rule between the two kernels would
 // cost a tile of 8 rows registers that it does not have: 96 bytes of spills, 6 us of 134).
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
     SeqInfo q = seq_info(S, b);
 
     int *const counters = static_cast<int *>(a.ws);
-    float *const parts = reinterpret_cast<float *>(counters + ((gridDim.x + 63) & ~63u));
+    float *const parts = reinterpret_cast<float *>(counters + stream_counters((int)gridDim.x, NT));
     constexpr int kPart = R * (D + 2);
 
     while (u < u1) {
@@ -1331,7 +1339,7 @@ static AttnPlan attn_plan(const AttnArgs &a, int sms) {
     p.streamed = !(p.tiled && a.s.batch == 1 && most > kManyRows);
     p.nt = stream_tiles(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
     const int64_t grid = (int64_t)sms * stream_ctas(p.nt);
-    p.stream_floats = (grid + 63) / 64 * 64 + 2 * grid * (8 * p.nt) * (a.c.dim + 2);
+    p.stream_floats = stream_counters((int)grid, p.nt) + 2 * grid * (8 * p.nt) * (a.c.dim + 2);
     p.pairs = prompt_pairs(a.s.tokens, a.s.batch, a.q_heads, a.c.heads);
     p.split = p.tiled ? prompt_split(p.pairs, longest, sms) : 1;
     return p;

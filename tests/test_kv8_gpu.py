@@ -564,6 +564,48 @@ def test_attention_bits_do_not_change_between_runs_and_the_workspace_is_reused()
     _check_attention(paged, q, out, lse, news, True, 128 ** -0.5)
 
 
+def test_attention_one_workspace_for_calls_of_all_shapes():
+    """Tiles of 8 and of 16 rows, many of them cut, and prompts with shared passes, one after another on one workspace of
+    the largest size: each gives what it gives on its own."""
+    hq, hk, dim = 16, 2, 128
+    paged = Paged([9000, 7000], hk, dim, 64)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)        # noqa: E731
+    jobs = {}
+    for name, lens, news, cu in (("pairs", [9000, 7000], [2, 2], ints(0, 2, 4)), ("single", [9000, 7000], [1, 1], None),
+                                 ("chunk", [9000], [24], ints(0, 24)), ("mixed", [9000, 3000], [40, 1], ints(0, 40, 41))):
+        q = _randn(sum(news), hq, dim, seed=len(jobs)) * 2
+        kv = ints(*lens)
+        table = paged.table_dev[:len(lens)]
+        own = cr.attn_kv8(q, paged.cache, table, kv, cu)
+        paged.lens = lens
+        _check_attention(paged, q, *own, news, True, dim ** -0.5, rows=3)
+        out, lse = torch.empty_like(own[0]), torch.empty_like(own[1])
+        jobs[name] = own, out, lse, (q, paged.cache, table, kv, out), dict(cu=cu, lse=lse)
+    size = max(cr.AttnKV8(*j[3], **j[4]).ws_bytes for j in jobs.values())
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    calls = {name: cr.AttnKV8(*j[3], **j[4], ws=ws) for name, j in jobs.items()}
+    order = ["pairs", "single", "pairs", "chunk", "single", "mixed", "single", "chunk", "pairs", "mixed", "pairs", "single"]
+    for name in order:
+        own, out, lse = jobs[name][:3]
+        out.zero_()
+        lse.zero_()
+        calls[name]()
+        assert torch.equal(out, own[0]) and torch.equal(lse, own[1]), name
+    # and as captured steps that are replayed in turn
+    graphs = {}
+    for name in jobs:
+        graphs[name] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[name]):
+            calls[name]()
+    for name in order:
+        own, out, lse = jobs[name][:3]
+        out.zero_()
+        lse.zero_()
+        graphs[name].replay()
+        assert torch.equal(out, own[0]) and torch.equal(lse, own[1]), name
+    cr.convrot_device_status()
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [200, 1, 30]])
 def test_a_captured_step_follows_its_tensors(news):
     """Append and attention in one CUDA graph: replays take new lengths and values from the same tensors."""
