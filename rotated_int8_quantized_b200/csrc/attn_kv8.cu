@@ -768,7 +768,8 @@ __device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 
 // Sequence b owns the slots from floor(cu[b] group / 256) + b on, at least as
-// many as it has pairs of tiles.  Called by a whole warp; -1: none.
+// many as it has pairs of tiles.  Called by a whole warp; -1: none.  within < 0
+// where cu decreases.
 __device__ __forceinline__ int find_slot(const AttnArgs &a, int64_t slot, int &within) {
     const int group = a.q_heads / a.c.heads;
     auto first_slot = [&](int i) {
@@ -786,7 +787,7 @@ __device__ __forceinline__ bool prompt_tile(const AttnArgs &a, int b, int slot, 
     t.q = seq_info(a.s, b);
     t.rows = (int64_t)t.q.n * group;
     t.row0 = (int64_t)slot * kPromptRows;
-    if (t.row0 >= t.rows || (!all && few_rows(t.rows, t.q.len, a))) return false;
+    if (slot < 0 || t.row0 >= t.rows || (!all && few_rows(t.rows, t.q.len, a))) return false;
     // what the last row sees is what any row sees
     const int64_t tok = (min(t.rows, t.row0 + kPromptRows) - 1) / group;
     const int64_t most = a.causal ? max((int64_t)0, min((int64_t)t.q.len, (int64_t)t.q.len - t.q.n + tok + 1)) : t.q.len;

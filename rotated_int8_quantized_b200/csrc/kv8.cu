@@ -52,6 +52,8 @@ struct TokenPlace {
 
 // The last b in [0, batch) with key(b) <= x, for key monotone in b; -1 if
 // there is none.  L consecutive lanes search together, L probes a step.
+// Where key is not monotone (a cu that decreases) some b of [0, batch), whose
+// key may be above x: callers that count from key(b) check that.
 template <int L, typename Key>
 __device__ __forceinline__ int search_lanes(int batch, int64_t x, Key key) {
     const int lane = threadIdx.x & (L - 1);
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
         t0 = __ldg(a.s.cu + b);
         n = (int64_t)__ldg(a.s.cu + b + 1) - t0;
         j = slot - ((t0 >> 4) + 2 * (int64_t)b);
-        if (t0 < 0 || n < 0 || t0 + n > a.s.tokens) {
+        if (t0 < 0 || n < 0 || t0 + n > a.s.tokens || j < 0) {       // j < 0: cu decreases
             if (threadIdx.x == 0) report_invalid();
             return;
         }

@@ -545,6 +545,37 @@ def test_attention_bad_device_arguments_are_recorded():
                 cr.convrot_device_status()
 
 
+@pytest.mark.parametrize("cu", [[0, 12000, 13000, 14000, 0, 0], [0, 12000, 13000, 14000, -2000, 0], [0, 9000, 200, 13000, 100, 14000],
+                                [13000, 0, 14000, 5, 14000, 6]])
+def test_a_decreasing_cu_stays_in_bounds(cu):
+    """Out of contract, recorded, and nothing beside the rows of the call and the sequences' own tokens is written."""
+    batch, tokens, hq, hk, dim, page = 5, 14000, 8, 1, 64, 64
+    wide = 16
+    paged = Paged([wide * page] * batch, hk, dim, page, spare=6)
+    cache = paged.cache
+    table = paged.table_dev[:, :wide].contiguous()
+    used = torch.zeros(cache.k.shape[0], dtype=torch.bool, device=DEV)
+    used[table.flatten().long()] = True
+    cu, kv = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (cu, [1000] * batch))
+    k, v = _randn(tokens, hk, dim), _randn(tokens, hk, dim, seed=1)
+    before = [x[~used].clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    cr.kv8_append(None, k, v, cache, table, kv, cu)
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+    for x, y in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+        assert torch.equal(x.nan_to_num(7), y[~used].nan_to_num(7))
+    room = torch.full((tokens + 8192, hq, dim), 5.0, dtype=torch.bfloat16, device=DEV)
+    out, lse = room[4096:4096 + tokens], torch.zeros(tokens, hq, device=DEV)
+    cr.AttnKV8(_randn(tokens, hq, dim), cache, table, kv, out, cu=cu, lse=lse)()
+    assert (room[:4096] == 5).all() and (room[4096 + tokens:] == 5).all()
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+    read = torch.full((tokens + 8192, hk, dim), 5.0, dtype=torch.bfloat16, device=DEV)
+    cr.KV8Read(cache, table, kv, read[4096:4096 + tokens], None, cu=cu)()
+    assert (read[:4096] == 5).all() and (read[4096 + tokens:] == 5).all()
+    cr.load_library().convrot_device_status(None)
+
+
 def test_attention_bits_do_not_change_between_runs_and_the_workspace_is_reused():
     lens, news = [3000, 10, 700], [1, 1, 1]
     paged = Paged(lens, 2, 128, 64)
