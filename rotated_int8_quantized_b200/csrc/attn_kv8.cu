@@ -1105,7 +1105,9 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         };
         auto finish = [&] {
             if (sc < 0) return;
-            const float ve = fmaxf(about.y, kLeastScale);
+            // finite even where the scale is not: a row that does not see the block has -infinity for its scores, and the
+            // sum with an infinite logarithm would be NaN
+            const float ve = fminf(fmaxf(about.y, kLeastScale), 3.40282347e38f);
             about.y = log2f(ve);
             about.z = 1.f / ve;
         };

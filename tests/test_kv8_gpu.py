@@ -498,6 +498,23 @@ def test_attention_a_nan_query_stays_in_its_row():
         assert torch.equal(out2[~hit], out[~hit]) and torch.equal(lse2[~hit], lse[~hit])
 
 
+@pytest.mark.parametrize("lens,news,hidden", [([98], [4], 2), ([200], [200], 160), ([4000], [24], 8), ([1000], [517], 29)])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_attention_rows_do_not_feel_what_they_do_not_see(lens, news, hidden, which, value):
+    """A later block whose scale is not finite: the `hidden` rows in front of it give what they gave."""
+    paged = Paged(lens, 1, 128, 16)
+    q = _randn(news[0], 8, 128)
+    cu = torch.tensor([0, news[0]], dtype=torch.int32, device=DEV)
+    out, lse = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu)
+    first = lens[0] - news[0] + hidden                       # the block's first token
+    assert first % BLOCK == 0
+    scales = paged.cache.k_scale if which == "k" else paged.cache.v_scale
+    scales[int(paged.table[0, first // 16]), 0, 0] = value
+    out2, lse2 = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu)
+    assert torch.equal(out2[:hidden], out[:hidden]) and torch.equal(lse2[:hidden], lse[:hidden])
+
+
 def test_attention_strided_queries_and_rows_behind():
     hq, hk, dim = 8, 2, 128
     paged = Paged([150, 33], hk, dim, 32)
