@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // 2^(14 - e), e the exponent of the row's largest element (held to what FP32 can scale by)
             int e = (int)(__float_as_uint(top) >> 23) - 127;
-            e = e > 127 ? 0 : (e < -100 ? -100 : e);
-            const float up = __int_as_float((127 + 14 - e) << 23);
+            const bool finite = e <= 127;                // a row with an infinity becomes NaN, whatever it meets
+            e = e < -100 ? -100 : e;
+            const float up = finite ? __int_as_float((127 + 14 - e) << 23) : __int_as_float(0x7FC00000);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -884,8 +885,9 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
                     top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
             }
             int e = (int)(__float_as_uint(top) >> 23) - 127;
-            e = e > 127 ? 0 : (e < -100 ? -100 : e);
-            const float up = __int_as_float((127 + 14 - e) << 23);
+            const bool finite = e <= 127;                // a row with an infinity becomes NaN, whatever it meets
+            e = e < -100 ? -100 : e;
+            const float up = finite ? __int_as_float((127 + 14 - e) << 23) : __int_as_float(0x7FC00000);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
                 const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};

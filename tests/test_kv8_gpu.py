@@ -515,6 +515,24 @@ def test_attention_rows_do_not_feel_what_they_do_not_see(lens, news, hidden, whi
     assert torch.equal(out2[:hidden], out[:hidden]) and torch.equal(lse2[:hidden], lse[:hidden])
 
 
+@pytest.mark.parametrize("lens,news", [([5], [1]), ([70], [3]), ([200], [200]), ([3000], [24])])
+def test_attention_an_infinite_query_never_counts_as_unseen(lens, news):
+    """A query whose scores are all -infinity (no codes of the other sign or zero in its way) is no row that sees nothing."""
+    paged = Paged(lens, 1, 128, 16)
+    paged.cache.k[..., 7] = 50
+    q = _randn(news[0], 8, 128)
+    cu = torch.tensor([0, news[0]], dtype=torch.int32, device=DEV)
+    out, lse = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu)
+    bad = q.clone()
+    bad[0, 1, 7] = float("-inf")
+    bad[-1, 6, 7] = float("-inf")
+    out2, lse2 = cr.attn_kv8(bad, paged.cache, paged.table_dev, paged.kv_len, cu)
+    hit = torch.zeros(out.shape[:2], dtype=torch.bool, device=DEV)
+    hit[0, 1] = hit[-1, 6] = True
+    assert out2[hit].isnan().all() and lse2[hit].isnan().all()
+    assert torch.equal(out2[~hit], out[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
 def test_attention_strided_queries_and_rows_behind():
     hq, hk, dim = 8, 2, 128
     paged = Paged([150, 33], hk, dim, 32)
