@@ -192,14 +192,18 @@ __device__ __forceinline__ uint2 pack_piece(const Row8 &r, int piece) {
 // coefficients in one: with P and Q the two values of four rotated pairs (two
 // at a time), P' = P c1 - Q s1 and Q' = Q c2 + P s2, where c1 = w_P cos, s1 = w_Q
 // sin, c2 = w_Q cos, s2 = w_P sin.  P and Q are the pieces (Adjacent: the even
-// and odd elements of a piece).
+// and odd elements of a piece).  A lane whose dims are not rotated only
+// multiplies by the weights (c1 and c2): 0 times an infinity in the partner
+// would be NaN.
 struct Turns {
     uint64_t c1[2], s1[2], c2[2], s2[2];
+    bool rotated;
 };
 
 template <bool Adjacent>
-__device__ __forceinline__ Turns make_turns(const float (&w)[8], const float (&c)[4], const float (&s)[4]) {
+__device__ __forceinline__ Turns make_turns(const float (&w)[8], const float (&c)[4], const float (&s)[4], bool rotated) {
     Turns t;
+    t.rotated = rotated;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         // elements of P and Q, and their pairs' numbers
@@ -233,9 +237,10 @@ __device__ __forceinline__ void norm_rotate(Row8 &x, const Turns &t, bool norm, 
         for (int k = 0; k < 2; ++k) x.e[k] = mul_f32x2(x.e[k], r2), x.o[k] = mul_f32x2(x.o[k], r2);
     }
     auto turn = [](uint64_t &p, uint64_t &q, const Turns &t, int k) {
-        const uint64_t u = fma_f32x2(q, t.s1[k], mul_f32x2(p, t.c1[k]));
-        q = fma_f32x2(p, t.s2[k], mul_f32x2(q, t.c2[k]));
+        uint64_t u = mul_f32x2(p, t.c1[k]), v = mul_f32x2(q, t.c2[k]);
+        if (t.rotated) u = fma_f32x2(q, t.s1[k], u), v = fma_f32x2(p, t.s2[k], v);
         p = u;
+        q = v;
     };
     if (Adjacent) {
         turn(x.e[0], x.o[0], t, 0);
@@ -286,7 +291,7 @@ __device__ __forceinline__ void head_rows(const HeadRows &in, const HeadRowsOut 
     load_weight(weight, g, w);
     const int what = rotation(c, s);
     if (what < 0) return;
-    const Turns turns = make_turns<Adjacent>(w, c, s);
+    const Turns turns = make_turns<Adjacent>(w, c, s, g.rotated);
     for (int h = h0; h < h1; h += 2) {
         Row8 y[2] = {unpack_row(x[0][0], x[0][1]), unpack_row(x[1][0], x[1][1])};
         load(h + 2);
@@ -517,7 +522,7 @@ __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid
     if (fresh) {
         ok = all_lanes<L>(ok);
         Row8 y = unpack_row(x[0], x[1]);
-        norm_rotate<L, Adjacent>(y, make_turns<Adjacent>(w, c, s), a.kw != nullptr, a.eps);
+        norm_rotate<L, Adjacent>(y, make_turns<Adjacent>(w, c, s, g.rotated), a.kw != nullptr, a.eps);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             row_piece(y, i, k[i]);

@@ -78,6 +78,37 @@ def test_single_rows_with_odd_strides():
     assert torch.equal(out, cr.attn_kv8(base, paged.cache, paged.table_dev, paged.kv_len)[0])
 
 
+def _bits(x):
+    return x.contiguous().view(torch.int16)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rot", [0, 8, 32])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_dims_without_rotation_stay_apart(dim, rot, adjacent):
+    """Infinities, NaN and the sign of a zero stay where they are in the dims that nothing turns."""
+    q = _randn(5, 3, dim)
+    for i, value in enumerate((float("inf"), float("-inf"), float("nan"), -0.0)):
+        q[i, 1, dim - 1 - 3 * i] = value
+        q[i, 2, rot + 2 * i] = value
+    rope = cr.Rope(cr.rope_table(9, rot), adjacent) if rot else None
+    pos = torch.arange(5, dtype=torch.int32, device=DEV) if rot else None
+    out, _ = cr.qk_norm_rope(q, rope=rope, positions=pos)
+    x, y = q[..., rot:], out[..., rot:]
+    assert torch.equal(x.isnan(), y.isnan()) and torch.equal(_bits(x)[~x.isnan()], _bits(y)[~x.isnan()])
+    if rot:
+        clean = q.clone()
+        clean[..., rot:] = 1
+        assert torch.equal(out[..., :rot], cr.qk_norm_rope(clean, rope=rope, positions=pos)[0][..., :rot])
+    # normalised by an infinite mean: zeros, and NaN where the infinity was
+    w = _randn(dim, seed=1)
+    out, _ = cr.qk_norm_rope(q[:2], None, w, rope=rope, positions=None if pos is None else pos[:2])
+    for i in range(2):
+        for h, d in ((1, dim - 1 - 3 * i), (2, rot + 2 * i)):
+            assert out[i, h].isnan().nonzero().flatten().tolist() == [d]
+            assert (out[i, h].nan_to_num() == 0).all()
+
+
 def test_norm_only_and_broadcast_input():
     q = _randn(1, 1, 64).expand(9, 3, 64)
     w = _randn(64, seed=2)
