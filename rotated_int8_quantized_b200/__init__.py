@@ -652,6 +652,8 @@ class _Prepared:
     on the tensors' own device.  The tensors stay the caller's: new values
     in them are what the next call works on."""
     _entry = ""
+    _cleared = None                       # event behind the clearing of a workspace that the call made itself,
+    _behind: set = frozenset()            # and the streams whose work is ordered behind it
 
     def _prepare(self, job, device: torch.device, *more) -> None:
         self.device = device
@@ -668,6 +670,8 @@ class _Prepared:
             handle = torch._C._cuda_getCurrentRawStream(index)
         else:
             handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if self._cleared is not None and handle not in self._behind:
+            self._wait_for_clear(handle)
         status = self._call(*self._args, handle)
         if status:
             _check(status, self._entry)
@@ -760,10 +764,27 @@ class AttnKV8(_Prepared):
             self.ws_bytes = int(load_library().convrot_attn_kv8_workspace_bytes(ctypes.byref(j)))
         if ws is None:
             # an invalid job needs none: the call says what is wrong with it
-            ws = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
+            with torch.cuda.device(device):
+                ws = torch.zeros(max(self.ws_bytes, 256), dtype=torch.uint8, device=device)
+                if not torch.cuda.is_current_stream_capturing():             # a graph clears it in its own order
+                    self._cleared = torch.cuda.Event()
+                    self._cleared.record()
+                    self._behind = {torch._C._cuda_getCurrentRawStream(device.index)}
         self.ws = ws
         self.keep = [q, cache, page_table, kv_len, out, cu, lse]
         self._prepare(j, device, _ptr(ws), ws.numel() * ws.element_size())
+
+    def _wait_for_clear(self, handle: int) -> None:
+        """Another stream's first call waits until the workspace made here is
+        cleared.  A stream that is being captured cannot wait for work outside
+        its graph: torch.cuda.graph has synchronised the device before."""
+        with _allocating(handle, self.device):
+            if torch.cuda.is_current_stream_capturing():
+                return
+            side = torch.cuda.current_stream()
+            side.wait_event(self._cleared)
+            self.ws.record_stream(side)
+        self._behind.add(handle)
 
 
 def _allocating(stream, device):

@@ -795,6 +795,55 @@ def test_two_streams_at_once():
         assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
 
 
+def test_a_first_call_on_another_stream_finds_its_workspace_cleared():
+    """The workspace that AttnKV8 makes is cleared on the stream of its construction, here far behind."""
+    paged = Paged([9000, 7000], 2, 128, 64)
+    q = _randn(2, 16, 128)
+    want, want_lse = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len)
+    out, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+    size = cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, lse=lse).ws_bytes
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        out.zero_()
+        lse.zero_()
+        used = torch.full((size,), 0x3F, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)                       # about a tenth of a second
+        del used
+        call = cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, lse=lse)
+        call(side)
+        call(side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    # made on a side stream, first called on the default one; and one that is first called in a capture
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        call = cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, lse=lse)
+    out.zero_()
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    call = cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        inside, _ = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len)
+    for _ in range(2):
+        out.zero_()
+        inside.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(inside, want)
+        out.zero_()
+        torch.cuda.synchronize()
+        call(side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_offsets_beyond_32_bits():
     """Codes of the last pages lie more than 2^32 bytes into the cache."""
     hk, dim, page = 8, 128, 128
