@@ -823,9 +823,10 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         return;
     }
     PromptTile tile;
-    if (!prompt_tile(a, b, sm.slot, all, tile)) return;
+    const bool has_rows = prompt_tile(a, b, sm.slot, all, tile);
     const SeqInfo &q = tile.q;
-    if (q.bad && tid == 0) report_invalid();
+    if (q.bad && tid == 0) report_invalid();         // also where no row is left of it
+    if (!has_rows) return;
     const int64_t rows = tile.rows, row0 = tile.row0;
     const int tiles = rows - row0 > 128 ? 2 : 1;
     // this CTA's range of the pass

@@ -609,6 +609,8 @@ __global__ void __launch_bounds__(kHeadThreads) kv8_read_kernel(const __grid_con
     const int64_t task = (int64_t)blockIdx.x * (kHeadThreads / L) + threadIdx.x / L;
     const int64_t t = task / chunks;
     if (t >= a.s.tokens) return;
+    // cu that is no partition of the rows: seen by one thread, whether or not a row meets it
+    if (a.s.cu && task == 0 && lane == 0 && (__ldg(a.s.cu) != 0 || __ldg(a.s.cu + a.s.batch) > a.s.tokens)) report_invalid();
     const TokenPlace p = place_token<L>(a.s, t);
     if (p.b < 0) return;
     const int H = a.c.heads, D = 8 * L;

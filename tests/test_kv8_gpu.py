@@ -642,6 +642,24 @@ def test_a_decreasing_cu_stays_in_bounds(cu):
     cr.load_library().convrot_device_status(None)
 
 
+@pytest.mark.parametrize("cu", [[0, 60, 200], [-4, 60, 130], [3, 60, 130], [0, 130, 131], [-9, 0, 130]])
+def test_read_records_rows_that_are_no_partition(cu):
+    paged = Paged([100, 130], 2, 64, 16)
+    out = torch.zeros(130, 2, 64, dtype=torch.bfloat16, device=DEV)
+    cr.KV8Read(paged.cache, paged.table_dev, paged.kv_len, out, None, cu=torch.tensor(cu, dtype=torch.int32, device=DEV))()
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+
+
+def test_attention_records_a_bad_cu_that_leaves_no_rows():
+    paged = Paged([100], 1, 64, 16)
+    for tokens in (1, 700):
+        q = _randn(tokens, 8, 64)
+        cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, torch.tensor([0, -5], dtype=torch.int32, device=DEV))
+        with pytest.raises(cr.ConvrotError):
+            cr.convrot_device_status()
+
+
 def test_attention_bits_do_not_change_between_runs_and_the_workspace_is_reused():
     lens, news = [3000, 10, 700], [1, 1, 1]
     paged = Paged(lens, 2, 128, 64)
