@@ -219,6 +219,75 @@ def _roomy(lens, need, hk, dim, page, seed=0):
     return paged
 
 
+@pytest.mark.parametrize("dim,rot", [(128, 128), (128, 64), (128, 8), (64, 64), (64, 24)])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("axes", [0, 1, 3])
+def test_append_rotations(dim, rot, adjacent, axes):
+    """Adjacent pairs, rotation of a part of the head, positions given (axes of them) or the cache's own."""
+    hq, hk, page = 5, 2, 32
+    lens, news = [0, 5, 16, 100, 0, 40], [3, 1, 33, 28, 0, 7]
+    paged = _roomy(lens, [a + b for a, b in zip(lens, news)], hk, dim, page)
+    old, total = list(lens), sum(news)
+    g = torch.Generator().manual_seed(rot + axes)
+    table = cr.rope_table(150, rot, 1e4)
+    pos = torch.randint(0, 150, (axes, total), generator=g, dtype=torch.int32) if axes else \
+        torch.cat([torch.arange(a, a + n) for a, n in zip(old, news)]).int()[None]
+    axis = torch.randint(0, axes, (rot // 2,), generator=g, dtype=torch.uint8) if axes > 1 else None
+    rope = cr.Rope(table, adjacent, None if axis is None else axis.to(DEV))
+    qkv = _randn(total, hq + 2 * hk, dim, seed=dim + rot, outliers=True)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    wq, wk = _randn(dim, seed=8), _randn(dim, seed=9)
+    paged.lens = [a + b for a, b in zip(old, news)]
+    kv_len = torch.tensor(paged.lens, dtype=torch.int32, device=DEV)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV)
+    before = [x.clone() for x in (paged.cache.k, paged.cache.v, paged.cache.k_scale, paged.cache.v_scale)]
+    out = cr.kv8_append(q, k, v, paged.cache, paged.table_dev, kv_len, cu, wq, wk, 1e-5, rope, pos.to(DEV) if axes else None)
+    cs, ax = table.cpu().numpy().astype(np.float64), None if axis is None else axis.numpy()
+    qr, kr = (norm_rotate(bits_to_f64(x), bits_to_f64(w), 1e-5, cs, pos.numpy(), ax, adjacent) for x, w in ((q, wq), (k, wk)))
+    _near_bf16(out, qr, np.abs(qr).max(-1, keepdims=True))
+    _check_append(paged, news, kr, bits_to_f64(v), old, before)
+    cr.convrot_device_status()
+
+
+def test_append_single_tokens_with_positions_of_three_axes():
+    """As a video model's decode step takes them; one of the four slots idle, one with a position outside the table."""
+    hq, hk, dim = 4, 1, 64
+    paged = _roomy([0, 7, 31, 0], [16, 16, 48, 16], hk, dim, 16)
+    q, k, v = (_randn(4, h, dim, seed=h + 1) for h in (hq, hk, hk))
+    table = cr.rope_table(40, dim, 1e4)
+    axis = (torch.arange(dim // 2) % 3).to(torch.uint8)
+    pos = torch.tensor([[3, 9, 11, 5], [0, 39, 2, 5], [7, 1, 40, 5]], dtype=torch.int32)
+    kv_len = torch.tensor([1, 8, 32, 0], dtype=torch.int32, device=DEV)
+    paged.lens = kv_len.tolist()
+    before = [x.clone() for x in (paged.cache.k, paged.cache.v, paged.cache.k_scale, paged.cache.v_scale)]
+    out = cr.kv8_append(q, k, v, paged.cache, paged.table_dev, kv_len, rope=cr.Rope(table, True, axis.to(DEV)),
+                        positions=pos.to(DEV))
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+    pos[2, 2] = 0                                            # the row written as zeros, see below
+    qr, kr = (norm_rotate(bits_to_f64(x), None, 0, table.cpu().numpy().astype(np.float64), pos.numpy(), axis.numpy(), True)
+              for x in (q, k))
+    qr[2:], kr[2] = 0, 0
+    _near_bf16(out, qr, np.abs(qr).max(-1, keepdims=True))
+    _check_append(paged, [1, 1, 1, 0], kr[:3], bits_to_f64(v)[:3], [0, 7, 31, 0], before)
+
+
+def test_append_rotates_queries_in_place():
+    hq, hk, dim, news = 6, 2, 128, [40, 1, 9]
+    paged = _roomy([3, 0, 20], [43, 1, 29], hk, dim, 16)
+    paged.kv_len = torch.tensor([43, 1, 29], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 40, 41, 50], dtype=torch.int32, device=DEV)
+    qkv, w, rope = _randn(50, hq + 2 * hk, dim), _randn(dim, seed=1), cr.Rope(cr.rope_table(50, dim), True)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    rest = qkv[:, hq:].clone()
+    want = cr.kv8_append(q, k, v, paged.cache, paged.table_dev, paged.kv_len, cu, w, w, rope=rope)
+    stored = [x.clone() for x in (paged.cache.k, paged.cache.v)]
+    cr.KV8Append(q, k, v, paged.cache, paged.table_dev, paged.kv_len, q, cu=cu, q_weight=w, k_weight=w, rope=rope)()
+    assert torch.equal(q, want) and torch.equal(qkv[:, hq:], rest)
+    assert torch.equal(stored[0], paged.cache.k) and torch.equal(stored[1], paged.cache.v)
+    cr.convrot_device_status()
+
+
 def test_append_token_by_token_stays_within_a_step():
     """Sixteen calls fill a block, every token larger than the last: each value ends within one step of its block's
     scale, the bound that doubling gives."""
@@ -660,6 +729,36 @@ def test_attention_records_a_bad_cu_that_leaves_no_rows():
             cr.convrot_device_status()
 
 
+@pytest.mark.parametrize("cu", [[0, 60, 200], [-4, 60, 130], [3, 60, 130], [0, 130, 131], [-9, 0, 130], [0, 130, 60]])
+def test_append_and_attention_record_rows_that_are_no_partition(cu):
+    paged = Paged([200, 200], 1, 64, 16)
+    cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    k, q = _randn(130, 1, 64), _randn(130, 4, 64)
+    cr.kv8_append(q, k, k, paged.cache, paged.table_dev, paged.kv_len, cu)
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+    cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu)
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+
+
+def test_a_length_beyond_the_table_is_recorded_by_every_call():
+    paged = Paged([100, 40], 2, 64, 16)
+    q, k = _randn(2, 8, 64), _randn(2, 2, 64)
+    kv = torch.tensor([2 ** 31 - 1, 40], dtype=torch.int32, device=DEV)
+    good, _ = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len)
+    for call in (lambda: cr.attn_kv8(q, paged.cache, paged.table_dev, kv), lambda: cr.kv8_read(paged.cache, paged.table_dev, kv),
+                 lambda: cr.kv8_append(q, k, k, paged.cache, paged.table_dev, kv)):
+        got = call()
+        with pytest.raises(cr.ConvrotError):
+            cr.convrot_device_status()
+        assert got[0].isfinite().all()
+    out, _ = cr.attn_kv8(q, paged.cache, paged.table_dev, kv)
+    assert torch.equal(out[1:], cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len)[0][1:]) and good.isfinite().all()
+    with pytest.raises(cr.ConvrotError):
+        cr.convrot_device_status()
+
+
 def test_attention_bits_do_not_change_between_runs_and_the_workspace_is_reused():
     lens, news = [3000, 10, 700], [1, 1, 1]
     paged = Paged(lens, 2, 128, 64)
@@ -887,6 +986,63 @@ def test_offsets_beyond_32_bits():
         out, lse = cr.attn_kv8(q, cache, table, kv, cu)
         small.lens = news
         _check_attention(small, q, out, lse, rows, True, dim ** -0.5, rows=3)
+
+
+def test_the_most_heads_and_eight_axes():
+    heads, dim = 4096, 64
+    x, w = _randn(3, heads, dim), _randn(dim, seed=1)
+    table = cr.rope_table(100, dim, 1e4)
+    pos = torch.randint(0, 100, (8, 3), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    axis = (torch.arange(dim // 2) % 8).to(torch.uint8)
+    rope = cr.Rope(table, False, axis.to(DEV))
+    ref = norm_rotate(bits_to_f64(x), bits_to_f64(w), 1e-6, table.cpu().numpy().astype(np.float64), pos.numpy(), axis.numpy(), False)
+    for y in cr.qk_norm_rope(x, x, w, w, rope=rope, positions=pos.to(DEV)):
+        _near_bf16(y, ref, np.abs(ref).max(-1, keepdims=True))
+    paged = _roomy([0], [3], heads, dim, 16)
+    q, k, v, _, old, before = _append(paged, [3], 0, heads, dim, 5)
+    _check_append(paged, [3], bits_to_f64(k), bits_to_f64(v), old, before)
+    cu = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    out, lse = cr.attn_kv8(x, paged.cache, paged.table_dev, paged.kv_len, cu)
+    _check_attention(paged, x, out, lse, [3], True, dim ** -0.5, rows=1)
+    # one key head for all of them: 4096 rows a token
+    _attend([37, 5], [2, 1], heads, 1, dim, 16, rows=1)
+    _attend([37], [1], heads, 1, dim, 16, cu=False)
+    cr.convrot_device_status()
+
+
+def test_shared_pages_and_a_sequence_taken_back():
+    """Two sequences with the same full pages in front, each with pages of its own behind; then one is taken back by some
+    tokens and appended to again."""
+    hk, dim, page = 2, 64, 32
+    paged = Paged([64 + 9, 64 + 30], hk, dim, page)
+    paged.table[1, :2] = paged.table[0, :2]
+    paged.table_dev = paged.table.to(DEV)
+    q, k, v, _, old, before = _append(paged, [5, 2], 0, hk, dim, 1)
+    _check_append(paged, [5, 2], bits_to_f64(k), bits_to_f64(v), old, before)
+    for news in ([1, 1], [60, 1]):
+        x = _randn(sum(news), 8, dim)
+        cu = torch.tensor([0, news[0], sum(news)], dtype=torch.int32, device=DEV)
+        out, lse = cr.attn_kv8(x, paged.cache, paged.table_dev, paged.kv_len, cu)
+        _check_attention(paged, x, out, lse, news, True, dim ** -0.5, rows=5)
+    paged.lens = [64 + 9 + 5 - 3, 64 + 32]
+    q, k, v, _, old, before = _append(paged, [8, 0], 0, hk, dim, 2)
+    _check_append(paged, [8, 0], bits_to_f64(k), bits_to_f64(v), old, before)
+    cr.convrot_device_status()
+
+
+def test_outputs_that_are_not_asked_for():
+    paged = Paged([100, 40], 2, 64, 16)
+    cu = torch.tensor([0, 90, 95], dtype=torch.int32, device=DEV)
+    k, v = cr.kv8_read(paged.cache, paged.table_dev, paged.kv_len, 95, cu)
+    for which, want in ((0, k), (1, v)):
+        got = torch.zeros_like(want)
+        cr.KV8Read(paged.cache, paged.table_dev, paged.kv_len, got if which == 0 else None, got if which else None, cu=cu)()
+        assert torch.equal(got, want)
+    q = _randn(95, 8, 64)
+    want, _ = cr.attn_kv8(q, paged.cache, paged.table_dev, paged.kv_len, cu)
+    out = torch.zeros_like(q)
+    cr.AttnKV8(q, paged.cache, paged.table_dev, paged.kv_len, out, cu=cu)()
+    assert torch.equal(out, want)
 
 
 def test_a_layer_from_projections_to_output():
