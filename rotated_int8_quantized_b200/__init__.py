@@ -723,6 +723,8 @@ class KV8Read(_Prepared):
 
     def __init__(self, cache: KV8Cache, page_table, kv_len, k_out, v_out, cu=None):
         h = cache.handle
+        if k_out is None and v_out is None:
+            raise ValueError("expected k_out, v_out or both")
         tokens = (k_out if k_out is not None else v_out).shape[0]
         j = self.job = convrot_kv8_read_t()
         j.cache = ctypes.pointer(h)

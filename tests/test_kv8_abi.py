@@ -211,3 +211,10 @@ def test_binding_refuses_wrong_tensors():
         cr.QKNormRope(x, None, x, None)
     with pytest.raises(ValueError):
         cr.QKNormRope(x.float(), None, x, None)
+
+
+def test_a_read_without_outputs_is_refused():
+    class Cache:
+        handle, k = _cache(), torch.zeros(1)
+    with pytest.raises(ValueError):
+        cr.KV8Read(Cache, torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), None, None)
