@@ -599,12 +599,15 @@ convrot_status_t convrot_qk_norm_rope(const convrot_qk_norm_rope_t *job, void *s
  *            size); so may whole sequences be empty.
  * A row whose position would be negative (kv_len[b] < n, an idle slot of a
  * captured batch) is padding: nothing is stored for it and its outputs are
- * zeros.  What only the device can see to be wrong (a page outside the cache
- * where one is needed, kv_len beyond max_pages * page_tokens, cu outside
- * 0 .. tokens) is recorded as CONVROT_ERR_INVALID_ARG for
- * convrot_device_status(); nothing is read or written out of bounds, tokens
- * on such pages are not stored, read as zeros and not attended to.  (A cu that
- * decreases is out of contract, but stays in bounds too.)
+ * zeros (but in attention without the causal mask positions do not matter:
+ * there it sees the kv_len tokens that every row sees).  What only the device
+ * can see to be wrong (a page outside the cache where one is needed, kv_len
+ * beyond max_pages * page_tokens, cu outside 0 .. tokens) is recorded as
+ * CONVROT_ERR_INVALID_ARG for convrot_device_status(); nothing is read or
+ * written out of bounds, tokens on such pages are not stored, read as zeros
+ * and not attended to, and the rows of a sequence whose kv_len or cu is wrong
+ * get unspecified values.  (A cu that decreases is out of contract; it stays in
+ * bounds and is recorded too.)
  */
 typedef struct {
     const int32_t *page_table, *kv_len, *cu;
@@ -677,7 +680,8 @@ convrot_status_t convrot_kv8_read(const convrot_kv8_read_t *job, void *stream);
  * Sums, maxima and accumulators are FP32; the weights of the value product
  * are FP16 (11 bits).  Scores (scale * q . K) stay below 2^24 in magnitude:
  * beyond that FP32 no longer tells neighbours apart.  A non-finite query gives
- * NaN in its own row only.
+ * NaN in its own row only, a block whose scale is not finite reaches only the
+ * rows that see it.  Value scales below 2^-100 count as 2^-100.
  * Results do not depend on the order in which the GPU runs the work.
  * Workspace: convrot_attn_kv8_workspace_bytes (0 if the job is invalid),
  * zero-filled before first use.  Every call leaves the counters at its front

@@ -740,7 +740,8 @@ class KV8Read(_Prepared):
 class AttnKV8(_Prepared):
     """Attention of q [tokens, q_heads, head_dim] over the cache into out
     (contiguous, BF16) and, if given, lse [tokens, q_heads] (fp32).  The
-    rows of sequence b are its last cu[b + 1] - cu[b] tokens.  ws: a
+    rows of sequence b are its last cu[b + 1] - cu[b] tokens; without
+    `causal` every one of them sees all kv_len[b].  ws: a
     workspace of at least `ws_bytes`, zero-filled before its first call
     (allocated here if None); AttnKV8 calls of any shapes may share one, but
     neither calls that run at the same time nor the linears' calls."""
@@ -811,7 +812,8 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, rop
 
 def kv8_append(q, k, v, cache: KV8Cache, page_table, kv_len, cu=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                rope: Optional[Rope] = None, positions=None, stream=None):
-    """KV8Append with a new q_out, which it returns (None without q)."""
+    """KV8Append with a new q_out, which it returns (None without q; rows
+    behind the last sequence hold anything)."""
     with _allocating(stream, k.device):
         q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
     KV8Append(q, k, v, cache, page_table, kv_len, q_out, cu, q_weight, k_weight, eps, rope, positions)(stream)

@@ -12,9 +12,11 @@
 // exact for every element above 2^-28 of the largest, off by 2^-39 of the
 // largest below that (a BF16 product would be no closer).  p' is held as FP16
 // scaled by 2^4: 11 bits where BF16 keeps 8, nothing above 2^-29 of the row's
-// maximum lost, and room for 2^11 more, so that the running maximum (and with
-// it all that was summed under it) is moved only when it falls that far behind.
-// Sums, maxima and accumulators are FP32.
+// maximum lost (fewer bits below 2^-18 of it), and room for 2^11 more, so that
+// the running maximum (and with it all that was summed under it) is moved only
+// when it falls behind: by a score 2^11 above it where rows are streamed, by a
+// step of 128 weights that sums to more than 2^15 (one score 2^11 above, or all
+// of them 2^4) in prompts.  Sums, maxima and accumulators are FP32.
 #include <cstdint>
 #include <type_traits>
 #include <cuda_bf16.h>
@@ -119,8 +121,6 @@ __device__ __forceinline__ uint2 ld_stream8(const void *p) {
     return v;
 }
 
-// Rows, cached tokens and first row of sequence b, held to the step's bounds
-// whatever the device arrays say.
 // An atomic add that orders this thread's (and, behind a barrier, its CTA's)
 // accesses on both sides of it.
 __device__ __forceinline__ int add_acq_rel(int *p, int v) {
@@ -135,6 +135,8 @@ __device__ __forceinline__ long long quotient(long long a, int b) {
     return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// Rows, cached tokens and first row of a sequence, held to the step's bounds
+// whatever the device arrays say.
 struct SeqInfo {
     int64_t t0;
     int n, len;
@@ -329,7 +331,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
             ks = __ldg(a.c.ks + sc);
             vs = __ldg(a.c.vs + sc);
         };
-        auto scales = [&] {                          // apart, so that nothing waits for them before the codes are asked for
+        // apart, so that nothing waits for them before the codes are asked for.  The quick logarithm (two units in its last
+        // place) moves a weight by 2^-20 of itself at usual scales and 2^-16 at the ends of the range, the quick quotient by
+        // 2^-22; a weight is rounded to 2^-12.
+        auto scales = [&] {
             const float ve = fmaxf(vs, kLeastScale);
             lv = __log2f(ve);
             iv = __fdividef(1.f, ve);
@@ -645,14 +650,15 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas(NT)) attn_strea
 //   12-15     one thread that issues the products; the others only give their
 //             registers away: a row's thread holds a step's 128 scores.
 // S = Q K^T (FP32, tensor memory) is read by the row's thread, and the weights
-// go back as FP16 over S and are the first operand of P V from there.  The second product sums in tensor
-// memory; as its scale (the running maximum) rarely moves by 2^8, the row's
-// thread rescales it in place when it does.  While one tile is in its softmax
+// go back as FP16 over S and are the first operand of P V from there.  The
+// second product sums in tensor memory; its scale (the running maximum) moves
+// only when a step's weights sum to more than 2^15, and the row's thread then
+// rescales it in place.  While one tile is in its softmax
 // the tensor cores work on the other.
 // K and V tiles are the same rows of 128 bytes (64 dims) in the 128-byte
 // swizzle; K is read along the dims (K-major), V along the tokens (MN-major).
-// Measured at 64 / 8 heads of 128: a prompt of 8192 tokens 1.19 .. 1.23 ms, 890 ..
-// 926 TFLOP/s of what is visible (55 % of the cuBLAS rate).  Of a step's 3850
+// Measured at 64 / 8 heads of 128: a prompt of 8192 tokens 1.20 .. 1.24 ms, 890 ..
+// 915 TFLOP/s of what is visible (55 % of the cuBLAS rate).  Of a step's 3850
 // clocks a tile spends 2100 in its softmax (of which 1024 are the exponentials'
 // at 8 clocks a warp and instruction; two warps at once would need 1275 each),
 // 1330 in its two products (1024 at full rate; the operands of Q K^T alone take

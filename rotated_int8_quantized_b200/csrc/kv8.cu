@@ -264,8 +264,8 @@ __device__ __forceinline__ void load_weight(const uint16_t *w, const LaneGeo &g,
 // Heads [h0, h1) of token row t: load, norm, rotate, round, store, two rows at
 // a time and the next two in flight.  Next to memory it is bound by what it
 // issues (one value at a time: 198 instructions a pair of rows, 79 % of the issue
-// slots, 83 us for 8191 tokens of 84 heads), hence the FP32 pairs: 74 us, 4.83
-// TB/s, 74 % of the copy rate.  `rotation` finds the coefficients once the first
+// slots, 83 us for 8191 tokens of 84 heads), hence the FP32 pairs: 75 us, 4.76
+// TB/s, 73 % of the copy rate.  `rotation` finds the coefficients once the first
 // rows are on their way, and says what to write: the rows (1), zeros (0) or
 // nothing (-1).  Rows may be rotated in place, so plain loads.
 template <int L, bool Adjacent, typename Rotation>
@@ -429,10 +429,11 @@ __device__ __forceinline__ float grow_scale(float most, bool held, float old, fl
 // values together (blockIdx.x < kv_ctas), or chunks of the queries' heads.
 // A block is one CTA's so that its scale needs no atomics and comes out the same
 // each time.  Measured: 5134 tokens of 5 sequences, 64 / 8 heads of 128 (200 MB)
-// 57 us, 54 % of the copy rate, bound by issue (a block's scale is worked out by
-// every one of its warps) and by the latency of search, length and coefficients
-// before a row is done; one token for each of 64 sequences is all latency (12 us
-// with the call that reads them back).
+// 59 us, 52 % of the copy rate; no unit is at its limit (issue slots 64 % busy, DRAM
+// 41 %): a CTA has one block of one head, and searches its sequence, length, page
+// and coefficients and has every warp work out the block's scale for it.  One
+// token for each of 64 sequences is all latency (13 us with the call that reads
+// them back).
 template <int L, bool Adjacent>
 __global__ void __launch_bounds__(16 * L, 64 / L) kv8_append_kernel(const __grid_constant__ AppendArgs a, int64_t kv_ctas, int per,
                                                           int chunks) {
