@@ -961,6 +961,37 @@ def test_a_first_call_on_another_stream_finds_its_workspace_cleared():
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_functions_on_another_stream(as_handle):
+    """stream= given as a stream or as its handle, the current stream far behind: what they make is made there."""
+    hq, hk, dim, news = 8, 2, 64, [50, 1, 3]
+    lens = [90, 700, 3]
+    paged = _roomy([a - b for a, b in zip(lens, news)], lens, hk, dim, 16)
+    paged.kv_len = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 50, 51, 54], dtype=torch.int32, device=DEV)
+    qkv, w, rope = _randn(54, hq + 2 * hk, dim), _randn(dim, seed=1), cr.Rope(cr.rope_table(700, dim))
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    pos = torch.arange(54, dtype=torch.int32, device=DEV)
+
+    def step(**on):
+        a, b = cr.qk_norm_rope(q, k, w, w, rope=rope, positions=pos, **on)
+        r = cr.kv8_append(q, k, v, paged.cache, paged.table_dev, paged.kv_len, cu, w, w, rope=rope, **on)
+        return [a, b, r, *cr.attn_kv8(r, paged.cache, paged.table_dev, paged.kv_len, cu, **on),
+                *cr.kv8_read(paged.cache, paged.table_dev, paged.kv_len, 54, cu, **on)]
+
+    want = [x.clone() for x in step()]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        got = step(stream=side.cuda_stream if as_handle else side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+        del got
+    cr.convrot_device_status()
+
+
 def test_offsets_beyond_32_bits():
     """Codes of the last pages lie more than 2^32 bytes into the cache."""
     hk, dim, page = 8, 128, 128
