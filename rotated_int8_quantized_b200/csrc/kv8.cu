@@ -429,8 +429,8 @@ __device__ __forceinline__ float grow_scale(float most, bool held, float old, fl
 // values together (blockIdx.x < kv_ctas), or chunks of the queries' heads.
 // A block is one CTA's so that its scale needs no atomics and comes out the same
 // each time.  Measured: 5134 tokens of 5 sequences, 64 / 8 heads of 128 (200 MB)
-// 59 us, 52 % of the copy rate; no unit is at its limit (issue slots 64 % busy, DRAM
-// 41 %): a CTA has one block of one head, and searches its sequence, length, page
+// 59 us, 52 % of the copy rate; no unit is at its limit (issue slots 66 % busy, DRAM
+// 40 %): a CTA has one block of one head, and searches its sequence, length, page
 // and coefficients and has every warp work out the block's scale for it.  One
 // token for each of 64 sequences is all latency (13 us with the call that reads
 // them back).
